@@ -16,7 +16,10 @@ Names and argument order follow the C ABI:
     qfused_pw_dw_forward,
     conv2d_status_string,
     conv2d_last_error
-plus ``make_params`` (keyword construction of a params struct).
+plus ``make_params`` (keyword construction of a params struct).  The operators
+of an attention layer (include/attention.h: linear_forward, qk_rope_forward,
+attention_forward and their descriptors) are bound in attention.py and exported
+here too.
 """
 import ctypes
 import math
@@ -429,5 +432,11 @@ def flops(params: conv2d_params_t) -> int:
     ho, wo = hnum // params.stride_h + 1, wnum // params.stride_w + 1
     return 2 * params.n * params.c_out * ho * wo * (params.c_in // params.groups) * params.k_h * params.k_w
 
+
+from .attention import (  # noqa: E402
+    attention_desc_create, attention_desc_destroy, attention_forward, attention_params_init, attention_params_t,
+    attention_workspace_bytes, linear_desc_create, linear_desc_destroy, linear_desc_kernel_name, linear_forward,
+    linear_params_init, linear_params_t, make_attention_params, make_linear_params, make_qk_rope_params,
+    qk_rope_desc_create, qk_rope_desc_destroy, qk_rope_forward, qk_rope_params_init, qk_rope_params_t)
 
 __all__ = [n for n in dir() if not n.startswith("_") and n not in ("ctypes", "math", "os")]

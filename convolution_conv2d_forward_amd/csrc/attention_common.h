@@ -1,0 +1,137 @@
+// Device helpers of the attention kernels: row intervals, scores, the join of
+// split results.
+//
+// Every mask of attention_forward leaves a query row one interval of keys:
+// documents and lengths bound it on both sides, a window on both, causal
+// order (with a prefix) above.  So a row carries [lo, hi) and nothing is read
+// per key.
+#pragma once
+
+#include "seq_common.h"
+
+namespace conv2d {
+
+struct SeqLens {
+    int nq, nk;   // rows of this sequence that count
+};
+
+__device__ __forceinline__ SeqLens seq_lens(const AttnArgs& a, int b) {
+    SeqLens s{a.q_len, a.kv_len};
+    if (a.q_lens) s.nq = min(max(a.q_lens[b], 0), a.q_len);
+    if (a.kv_lens) s.nk = min(max(a.kv_lens[b], 0), a.kv_len);
+    return s;
+}
+
+// The keys that query i of sequence b sees.  Empty: lo = hi = 0.
+__device__ __forceinline__ void row_interval(const AttnArgs& a, SeqLens s, int b, int i, int& lo, int& hi) {
+    const int p = s.nk - s.nq + i;
+    lo = 0;
+    hi = s.nk;
+    if (i >= s.nq) hi = 0;
+    if (a.causal) {
+        int end = p + 1;
+        if (a.prefix_lens) end = max(end, a.prefix_lens[b]);
+        hi = min(hi, end);
+    }
+    if (a.window) {
+        lo = (int)max((int64_t)lo, (int64_t)p - a.window + 1);
+        hi = (int)min((int64_t)hi, (int64_t)p + a.window);
+    }
+    if (a.doc_offsets) {
+        // The last document that starts at or before p: the number of
+        // borders <= p, by halving.  Offsets that do not ascend select some
+        // document; the interval stays within the sequence.
+        const int32_t* o = a.doc_offsets + (int64_t)b * (a.n_docs + 1);
+        int n0 = 0, n1 = a.n_docs + 1;
+        while (n0 < n1) {
+            const int mid = (n0 + n1) >> 1;
+            if (o[mid] <= p)
+                n0 = mid + 1;
+            else
+                n1 = mid;
+        }
+        if (n0 == 0 || n0 > a.n_docs || p < 0) {
+            hi = 0;
+        } else {
+            lo = max(lo, o[n0 - 1]);
+            hi = min(hi, o[n0]);
+        }
+    }
+    if (hi <= lo) lo = hi = 0;
+}
+
+// tanh to the last digits of its type's use: fp32 results take the library's,
+// bf16 ones 1 - 2 / (exp(2x) + 1), whose absolute error of some 2^-23 is far
+// below the weights' rounding to bf16.
+template <typename T>
+__device__ __forceinline__ float score_tanh(float x);
+template <>
+__device__ __forceinline__ float score_tanh<float>(float x) {
+    return tanhf(x);
+}
+template <>
+__device__ __forceinline__ float score_tanh<bf16>(float x) {
+    const float e = __builtin_amdgcn_exp2f(x * (2.0f * kLog2e));
+    return 1.0f - 2.0f * __builtin_amdgcn_rcpf(e + 1.0f);
+}
+
+// Scores in units of log 2, so that exp2 gives the weights.
+struct ScoreP {
+    float scale;   // without a cap: scale log2(e); with one: scale / cap
+    float cap;     // cap log2(e), 0 without
+};
+
+__device__ __forceinline__ ScoreP score_params(const AttnArgs& a) {
+    ScoreP p;
+    p.cap = a.softcap * kLog2e;
+    p.scale = a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e;
+    return p;
+}
+
+// Elements whose exponent bits are all ones (infinities, NaN) become zero;
+// says whether there were any.
+template <typename T>
+__device__ __forceinline__ bool clean_chunk(u32x4& v);
+template <>
+__device__ __forceinline__ bool clean_chunk<float>(u32x4& v) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if ((v[i] & 0x7f800000u) == 0x7f800000u) {
+            v[i] = 0;
+            bad = true;
+        }
+    return bad;
+}
+template <>
+__device__ __forceinline__ bool clean_chunk<bf16>(u32x4& v) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if ((v[i] & 0x7f80u) == 0x7f80u) {
+            v[i] &= 0xffff0000u;
+            bad = true;
+        }
+        if ((v[i] & 0x7f800000u) == 0x7f800000u) {
+            v[i] &= 0xffffu;
+            bad = true;
+        }
+    }
+    return bad;
+}
+
+// Partial results of a split: for each (sequence, key head, split, row)
+// d unnormalised outputs, then for all rows the pair (running maximum, sum).
+__device__ __forceinline__ int64_t ws_row(const AttnArgs& a, int bh, int split, int row) {
+    return ((int64_t)bh * a.splits + split) * a.rows + row;
+}
+__device__ __forceinline__ float* ws_out(const AttnArgs& a, int64_t row) { return a.ws + row * a.d; }
+__device__ __forceinline__ f32x2* ws_stat(const AttnArgs& a, int64_t row) {
+    const int64_t all = (int64_t)a.batch * a.heads_kv * a.splits * a.rows;
+    return (f32x2*)(a.ws + all * a.d) + row;
+}
+
+// Joins the splits' results (attention_any.hip).
+hipError_t launch_attention_join(int32_t dtype, const AttnArgs& a, hipStream_t s);
+
+}  // namespace conv2d

@@ -32,11 +32,9 @@ int conv2d::device_cu_count() {
     return n;
 }
 
-namespace {
+static thread_local char g_last_error[512] = "";
 
-thread_local char g_last_error[512] = "";
-
-conv_status_t fail(conv_status_t s, const char* fmt, ...) {
+conv_status_t conv2d::fail(conv_status_t s, const char* fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
     vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
@@ -44,10 +42,34 @@ conv_status_t fail(conv_status_t s, const char* fmt, ...) {
     return s;
 }
 
-conv_status_t ok() {
+conv_status_t conv2d::ok() {
     g_last_error[0] = '\0';
     return CONV_OK;
 }
+
+conv_status_t conv2d::hip_status(hipError_t e, const char* what) {
+    if (e == hipSuccess) return ok();
+    return fail(CONV_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+// Do two strided views overlap?  Both are lists of n equal-length blocks at a
+// constant stride; walk them in address order (two pointers, O(n1 + n2)).
+bool conv2d::views_overlap(const View& a, const View& b) {
+    if (a.len == 0 || b.len == 0 || a.n == 0 || b.n == 0) return false;
+    const uintptr_t a_end = a.base + (uintptr_t)((a.n - 1) * a.stride + a.len);
+    const uintptr_t b_end = b.base + (uintptr_t)((b.n - 1) * b.stride + b.len);
+    if (a_end <= b.base || b_end <= a.base) return false;
+    int64_t i = 0, j = 0;
+    while (i < a.n && j < b.n) {
+        const uintptr_t as = a.base + (uintptr_t)(i * a.stride), ae = as + (uintptr_t)a.len;
+        const uintptr_t bs = b.base + (uintptr_t)(j * b.stride), be = bs + (uintptr_t)b.len;
+        if (as < be && bs < ae) return true;
+        if (ae <= be) ++i; else ++j;
+    }
+    return false;
+}
+
+namespace {
 
 const char* kernel_name(const Desc& d) {
     switch (d.kclass) {
@@ -75,32 +97,6 @@ const char* kernel_name(const Desc& d) {
 
 size_t elem_size(int32_t dtype) {
     return dtype == CONV_DTYPE_F32 ? 4 : dtype == CONV_DTYPE_BF16 ? 2 : 1;
-}
-
-// Byte ranges of a tensor view: n blocks of `len` bytes, `stride` apart.
-struct View {
-    uintptr_t base;
-    int64_t n;
-    int64_t stride;
-    int64_t len;
-    int64_t first() const { return 0; }
-};
-
-// Do two strided views overlap?  Both are lists of n equal-length blocks at a
-// constant stride; walk them in address order (two pointers, O(n1 + n2)).
-bool views_overlap(const View& a, const View& b) {
-    if (a.len == 0 || b.len == 0 || a.n == 0 || b.n == 0) return false;
-    const uintptr_t a_end = a.base + (uintptr_t)((a.n - 1) * a.stride + a.len);
-    const uintptr_t b_end = b.base + (uintptr_t)((b.n - 1) * b.stride + b.len);
-    if (a_end <= b.base || b_end <= a.base) return false;
-    int64_t i = 0, j = 0;
-    while (i < a.n && j < b.n) {
-        const uintptr_t as = a.base + (uintptr_t)(i * a.stride), ae = as + (uintptr_t)a.len;
-        const uintptr_t bs = b.base + (uintptr_t)(j * b.stride), be = bs + (uintptr_t)b.len;
-        if (as < be && bs < ae) return true;
-        if (ae <= be) ++i; else ++j;
-    }
-    return false;
 }
 
 View flat(const void* p, int64_t bytes) { return View{(uintptr_t)p, 1, 0, bytes}; }
@@ -140,11 +136,6 @@ ConvArgs make_args(const Desc& d, const void* x, const void* w, const float* bia
     a.act = p.act_type; a.act_a = p.act_params[0]; a.act_b = p.act_params[1];
     a.slope_count = p.prelu_slope_count;
     return a;
-}
-
-conv_status_t hip_status(hipError_t e, const char* what) {
-    if (e == hipSuccess) return ok();
-    return fail(CONV_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
 conv_status_t check_desc(conv2d_desc_t d) {

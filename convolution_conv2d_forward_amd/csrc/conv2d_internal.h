@@ -11,6 +11,23 @@
 
 namespace conv2d {
 
+// Status of a call: fail() keeps the message for conv2d_last_error() on this
+// thread, ok() clears it, hip_status() is either, by e.
+conv_status_t fail(conv_status_t s, const char* fmt, ...);
+conv_status_t ok();
+conv_status_t hip_status(hipError_t e, const char* what);
+
+// Byte ranges of a tensor view: n blocks of `len` bytes, `stride` apart.
+struct View {
+    uintptr_t base;
+    int64_t n;
+    int64_t stride;
+    int64_t len;
+    int64_t first() const { return 0; }
+};
+
+bool views_overlap(const View& a, const View& b);
+
 // Kernel classes chosen by the descriptor.
 enum KernelClass : int32_t {
     KC_IGEMM_F32 = 0,    // implicit GEMM, fp32 MFMA (dense, grouped, pointwise)
