@@ -80,12 +80,13 @@ LinearArgs linear_args(const linear_params_t& p, int64_t rows, const void* x, co
     a.residual = p.has_residual ? residual : nullptr;
     a.xs = p.x_stride; a.ys = p.y_stride; a.rs = p.residual_stride;
     a.m = (int32_t)rows; a.k = p.k; a.n = p.n;
-    a.act = p.act_type; a.act_a = p.act_params[0]; a.act_b = p.act_params[1];
-    a.vec = p.k % chunk == 0 && p.x_stride % chunk == 0 && aligned16(x) && aligned16(w);
+    a.act = p.act_type; a.act_a = p.act_type == CONV_ACT_RELU ? 0.0f : p.act_params[0]; a.act_b = p.act_params[1];
+    a.vec = p.k % chunk == 0 && p.x_stride % chunk == 0 && aligned16(x) && aligned16(w) &&
+            (p.x_stride > p.k ? p.x_stride : p.k) * es * 256 < (int64_t)1 << 32;
     const auto out_ok = [&](const void* q, int64_t stride) {
-        return stride % 4 == 0 && ((uintptr_t)q & (uintptr_t)(4 * es - 1)) == 0;
+        return stride % chunk == 0 && aligned16(q);
     };
-    a.vec_out = p.n % 4 == 0 && out_ok(y, p.y_stride) && (!p.has_residual || out_ok(residual, p.residual_stride)) &&
+    a.vec_out = p.n % 8 == 0 && out_ok(y, p.y_stride) && (!p.has_residual || out_ok(residual, p.residual_stride)) &&
                 (!p.has_bias || aligned16(bias));
     return a;
 }

@@ -1,112 +1,58 @@
-// y = act(x w^T + bias) + residual: dispatch, and the kernel for any size,
-// stride and alignment.
+// Dispatch of linear_forward.
 #include "linear_common.h"
 
 namespace conv2d {
 
 namespace {
 
-// 16 bytes of a row from element k on, zero from a.k on.  vec: the chunk is
-// aligned, and wholly inside or outside.
-template <typename T>
-__device__ __forceinline__ u32x4 load_chunk(const T* row, int k, int kend, bool vec) {
-    constexpr int C = Vec<T>::chunk;
-    u32x4 r{0, 0, 0, 0};
-    if (vec) {
-        if (k < kend) r = *(const u32x4*)(row + k);
-        return r;
-    }
-    T e[C];
-#pragma unroll
-    for (int i = 0; i < C; ++i) e[i] = k + i < kend ? row[k + i] : (T)0.0f;
-    __builtin_memcpy(&r, e, 16);
-    return r;
-}
-
-// 64 rows of x by 64 rows of w per workgroup of four waves, each wave a 32x32
-// quarter; 128 bytes of every row a step through one LDS buffer, the next
-// step's chunks in registers meanwhile.  16-byte chunks are stored at
-// chunk ^ (row & 7), so the 16 rows that a wave reads at once lie in
-// different banks.
-template <typename T>
-__global__ __launch_bounds__(256) void linear_any(LinearArgs a, uint32_t tiles_n) {
-    constexpr int C = Vec<T>::chunk, BK = 8 * C;
-    __shared__ __align__(16) u32x4 lds[2][64 * 8];
-    const uint32_t b = xcd_remap(blockIdx.x, gridDim.x);
-    const int m0 = (int)(b / tiles_n) * 64, n0 = (int)(b % tiles_n) * 64;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-    // Thread's chunks: rows tid/8 and tid/8 + 32 of each tile, chunk tid % 8.
-    const int lr = tid >> 3, lc = tid & 7;
-    const T* xr[2];
-    const T* wr[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        int m = m0 + lr + 32 * i, n = n0 + lr + 32 * i;
-        m = m < a.m ? m : a.m - 1;   // rows past the end repeat the last one; their results are not stored
-        n = n < a.n ? n : a.n - 1;
-        xr[i] = (const T*)a.x + (int64_t)m * a.xs;
-        wr[i] = (const T*)a.w + (int64_t)n * a.k;
-    }
-    u32x4 rx[2], rw[2];
-    const auto fetch = [&](int k0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            rx[i] = load_chunk(xr[i], k0 + lc * C, a.k, a.vec);
-            rw[i] = load_chunk(wr[i], k0 + lc * C, a.k, a.vec);
+// The kernel of a call, by sizes and type alone.  Few rows go to linear_rows,
+// whose workgroups read 16 rows of w and all of x: up to 32 rows always, up to
+// 128 while x is not read too often (64x4096x4096: 14.8 us against 23.2 in
+// tiles; 64x4096x11264: 35.3 against 28.0).  Else the tile whose workgroups
+// are expected to end first: rounds of workgroups times the time of a step,
+// measured (us) with all CUs at work:
+//              256    128 by pairs    128 deep    64
+//   bf16       1.9    1.2             0.72        0.49, one a CU 0.30
+//   fp32       -      3.85            2.07        1.1, one a CU 0.65
+// (2048x4096x4096 bf16: 111 us in tiles of 256, 80 in pairs of 128, 93 in
+// deep ones, 129 in tiles of 64.)
+linear_tile_t pick(int32_t dtype, const LinearArgs& a) {
+    if (a.m <= 32) return LINEAR_ROWS;
+    if (a.m <= 128 && a.vec && (int64_t)((a.n + 15) / 16) * ((a.m + 15) / 16 + 1) <= 2304) return LINEAR_ROWS;
+    const int64_t cus = device_cu_count();
+    const auto rounds = [&](int64_t t, int64_t per_cu) {
+        const int64_t tiles = ((a.m + t - 1) / t) * ((a.n + t - 1) / t);
+        return (float)((tiles + cus * per_cu - 1) / (cus * per_cu));
+    };
+    const bool f32 = dtype == CONV_DTYPE_F32;
+    float best = rounds(64, 1) == 1 ? (f32 ? 0.65f : 0.30f) : rounds(64, 2) * (f32 ? 1.1f : 0.49f);
+    linear_tile_t tile = LINEAR_TILE_64;
+    const auto offer = [&](linear_tile_t t, float cost) {
+        if (cost < best) {
+            best = cost;
+            tile = t;
         }
     };
-    f32x4 acc[2][2] = {};
-    fetch(0);
-    for (int k0 = 0; k0 < a.k; k0 += BK) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = lr + 32 * i, at = row * 8 + (lc ^ (row & 7));
-            lds[0][at] = rx[i];
-            lds[1][at] = rw[i];
-        }
-        __syncthreads();
-        if (k0 + BK < a.k) fetch(k0 + BK);
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            const int c = ks * 4 + (lane >> 4), r = lane & 15;
-            u32x4 fw[2], fx[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int rw_ = wn + 16 * i + r, rx_ = wm + 16 * i + r;
-                fw[i] = lds[1][rw_ * 8 + (c ^ (rw_ & 7))];
-                fx[i] = lds[0][rx_ * 8 + (c ^ (rx_ & 7))];
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) acc[i][j] = mfma_step<T>(fw[i], fx[j], acc[i][j]);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            linear_store<T>(a, m0 + wm + 16 * j + (lane & 15), n0 + wn + 16 * i + 4 * (lane >> 4), acc[i][j]);
-}
-
-template <typename T>
-hipError_t run_any(const LinearArgs& a, hipStream_t s) {
-    const int64_t tm = ((int64_t)a.m + 63) / 64, tn = ((int64_t)a.n + 63) / 64;
-    if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
-    linear_any<T><<<dim3((uint32_t)(tm * tn)), dim3(256), 0, s>>>(a, (uint32_t)tn);
-    return hipGetLastError();
+    offer(LINEAR_TILE_128_DEEP, rounds(128, 1) * (f32 ? 2.07f : 0.72f));
+    offer(LINEAR_TILE_128, rounds(128, 2) * (f32 ? 3.85f : 1.2f));
+    if (!f32) offer(LINEAR_TILE_256, rounds(256, 1) * 1.9f);
+    return tile;
 }
 
 }  // namespace
 
 const char* linear_kernel_name(int32_t dtype, const LinearArgs& a) {
-    return dtype == CONV_DTYPE_F32 ? "linear_any_f32" : "linear_any_bf16";
+    static const char* const names[2][5] = {{"linear_rows_f32", "linear_tile_f32/64", "linear_tile_f32/128",
+                                             "linear_tile_f32/128deep", "linear_tile_f32/256"},
+                                            {"linear_rows_bf16", "linear_tile_bf16/64", "linear_tile_bf16/128",
+                                             "linear_tile_bf16/128deep", "linear_tile_bf16/256"}};
+    return names[dtype == CONV_DTYPE_F32 ? 0 : 1][pick(dtype, a)];
 }
 
 hipError_t launch_linear(int32_t dtype, const LinearArgs& a, hipStream_t s) {
-    return dtype == CONV_DTYPE_F32 ? run_any<float>(a, s) : run_any<bf16>(a, s);
+    const linear_tile_t tile = pick(dtype, a);
+    if (tile == LINEAR_ROWS) return launch_linear_rows(dtype, a, s);
+    return dtype == CONV_DTYPE_F32 ? launch_linear_tile<float>(a, tile, s) : launch_linear_tile<bf16>(a, tile, s);
 }
 
 }  // namespace conv2d

@@ -2,6 +2,8 @@
 // and the epilogue.
 #pragma once
 
+#include <type_traits>
+
 #include "seq_common.h"
 
 namespace conv2d {
@@ -28,52 +30,76 @@ __device__ __forceinline__ f32x4 mfma_step<float>(u32x4 a, u32x4 b, f32x4 c) {
     return c;
 }
 
-// erf(x) to fp32: the library's.  tanh(u) through 1 - 2 / (exp(2u) + 1) keeps
-// its absolute error near 2^-24, which is what (1 + tanh) is added to.
-__device__ __forceinline__ float linear_act(int act, float pa, float pb, float v) {
-    switch (act) {
-    case CONV_ACT_RELU:
-        return v > 0.0f ? v : v != v ? v : 0.0f;
-    case CONV_ACT_LEAKY_RELU:
-        return v >= 0.0f ? v : pa * v;
-    case CONV_ACT_CLIP:
-        return fminf(fmaxf(v, pa), pb);
-    case LINEAR_ACT_SILU:
-        return v / (1.0f + __expf(-v));
-    case LINEAR_ACT_GELU:
-        return 0.5f * v * (1.0f + erff(v * 0.70710678118654752440f));
-    case LINEAR_ACT_GELU_TANH: {
-        const float u = 0.79788456080286535588f * (v + 0.044715f * v * v * v);
-        return v - v / (1.0f + __expf(2.0f * u));
-    }
-    default:
-        return v;
+// Kinds of activation that kernels are compiled for: one kernel for all would
+// hold every activation's code once for each block of outputs, some 300 KB,
+// and wait for its instructions.
+enum { kActNone, kActPiecewise, kActSilu, kActGelu, kActGeluTanh };
+
+// The activation of N values.  tanh(u) through 1 - 2 / (exp(2u) + 1) keeps its
+// absolute error near 2^-24, which is what (1 + tanh) is added to.
+template <int KIND, int N>
+__device__ __forceinline__ void linear_act(const LinearArgs& a, float* v) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float x = v[i];
+        if constexpr (KIND == kActPiecewise) {
+            if (a.act == CONV_ACT_CLIP)
+                v[i] = fminf(fmaxf(x, a.act_a), a.act_b);
+            else   // RELU (act_a = 0) and LEAKY_RELU; NaN stays
+                v[i] = x > 0.0f ? x : a.act_a == 0.0f ? (x != x ? x : 0.0f) : a.act_a * x;
+        } else if constexpr (KIND == kActSilu) {
+            v[i] = x / (1.0f + __expf(-x));
+        } else if constexpr (KIND == kActGelu) {
+            v[i] = 0.5f * x * (1.0f + erff(x * 0.70710678118654752440f));
+        } else if constexpr (KIND == kActGeluTanh) {
+            const float u = 0.79788456080286535588f * (x + 0.044715f * x * x * x);
+            v[i] = x - x / (1.0f + __expf(2.0f * u));
+        }
     }
 }
 
-// Four outputs of row m, columns n .. n + 3 (those below a.n).
-template <typename T>
-__device__ __forceinline__ void linear_store(const LinearArgs& a, int m, int n, f32x4 v) {
-    typedef typename Vec<T>::v4 V;
-    if (m >= a.m || n >= a.n) return;
-    T* y = (T*)a.y + (int64_t)m * a.ys + n;
-    const T* r = a.residual ? (const T*)a.residual + (int64_t)m * a.rs + n : nullptr;
-    if (a.vec_out) {
-        f32x4 b{0, 0, 0, 0}, res{0, 0, 0, 0};
-        if (a.bias) b = *(const f32x4*)(a.bias + n);
-        if (r) res = to_f32(*(const V*)r);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = linear_act(a.act, a.act_a, a.act_b, v[i] + b[i]) + res[i];
-        *(V*)y = from_f32<T>(v);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (n + i >= a.n) break;
-        const float b = a.bias ? a.bias[n + i] : 0.0f;
-        const float res = r ? to_f32(r[i]) : 0.0f;
-        y[i] = from_f32<T>(linear_act(a.act, a.act_a, a.act_b, v[i] + b) + res);
+// Calls f with the kind of a's activation as a compile-time constant.
+template <typename F>
+hipError_t with_act(const LinearArgs& a, F f) {
+    switch (a.act) {
+    case CONV_ACT_NONE: return f(std::integral_constant<int, kActNone>{});
+    case LINEAR_ACT_SILU: return f(std::integral_constant<int, kActSilu>{});
+    case LINEAR_ACT_GELU: return f(std::integral_constant<int, kActGelu>{});
+    case LINEAR_ACT_GELU_TANH: return f(std::integral_constant<int, kActGeluTanh>{});
+    default: return f(std::integral_constant<int, kActPiecewise>{});
     }
 }
+
+// 16 bytes from p on at any alignment of the element, of which `left` elements
+// belong to the row: zero past them.
+template <typename T>
+__device__ __forceinline__ u32x4 load_chunk(const T* p, int left) {
+    constexpr int C = Vec<T>::chunk;
+    u32x4 r;
+    if (left >= C) {
+        __builtin_memcpy(&r, p, 16);
+        return r;
+    }
+    T e[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) e[i] = i < left ? p[i] : (T)0.0f;
+    __builtin_memcpy(&r, e, 16);
+    return r;
+}
+
+// Kernels of a call: few rows of x (linear_rows.hip), or tiles of as many rows
+// of x and w (linear_tile.h), 128 with two workgroups on a CU or with one and
+// a deeper pipeline.
+enum linear_tile_t { LINEAR_ROWS, LINEAR_TILE_64, LINEAR_TILE_128, LINEAR_TILE_128_DEEP, LINEAR_TILE_256 };
+
+// Up to 128 rows of x; those past 32 in rows that start at 16-byte boundaries.
+hipError_t launch_linear_rows(int32_t dtype, const LinearArgs& a, hipStream_t s);
+
+template <typename T>
+hipError_t launch_linear_tile(const LinearArgs& a, linear_tile_t tile, hipStream_t s);
+template <>
+hipError_t launch_linear_tile<float>(const LinearArgs& a, linear_tile_t tile, hipStream_t s);
+template <>
+hipError_t launch_linear_tile<bf16>(const LinearArgs& a, linear_tile_t tile, hipStream_t s);
 
 }  // namespace conv2d

@@ -1,0 +1,208 @@
+// y = act(x w^T + bias) + residual for few rows of x: bound by the bytes of w.
+#include "linear_common.h"
+
+namespace conv2d {
+
+namespace {
+
+// The activation, its kind at run time: for the few outputs of a thread here.
+template <int N>
+__device__ __forceinline__ void linear_act_any(const LinearArgs& a, float* v) {
+    switch (a.act) {
+    case CONV_ACT_NONE: break;
+    case LINEAR_ACT_SILU: linear_act<kActSilu, N>(a, v); break;
+    case LINEAR_ACT_GELU: linear_act<kActGelu, N>(a, v); break;
+    case LINEAR_ACT_GELU_TANH: linear_act<kActGeluTanh, N>(a, v); break;
+    default: linear_act<kActPiecewise, N>(a, v);
+    }
+}
+
+// The waves' sums meet in LDS, and 16 NT x 16 MT outputs from column n0 on are
+// formed and stored.
+template <typename T, int MT, int NT, int NW>
+__device__ __forceinline__ void rows_store(const LinearArgs& a, const f32x4 (&acc)[NT][MT], f32x4* red, int n0,
+                                           int wave, int lane) {
+    const int r = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) red[(wave * NT * MT + i * MT + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    for (int t = wave; t < NT * MT; t += NW) {
+        const int m = 16 * (t % MT) + r, n = n0 + 16 * (t / MT) + 4 * g;
+        if (m >= a.m || n >= a.n) continue;
+        T* y = (T*)a.y + m * a.ys + n;
+        const T* res = a.residual ? (const T*)a.residual + m * a.rs + n : nullptr;
+        f32x4 v = red[t * 64 + lane];
+#pragma unroll
+        for (int i = 1; i < NW; ++i) v += red[(i * NT * MT + t) * 64 + lane];
+        if (a.vec_out) {
+            if (a.bias) v += *(const f32x4*)(a.bias + n);
+            linear_act_any<4>(a, (float*)&v);
+            if (res) v += to_f32(*(const typename Vec<T>::v4*)res);
+            *(typename Vec<T>::v4*)y = from_f32<T>(v);
+            continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (a.bias && n + i < a.n) v[i] += a.bias[n + i];
+        linear_act_any<4>(a, (float*)&v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < a.n) y[i] = from_f32<T>(v[i] + (res ? to_f32(res[i]) : 0.0f));
+    }
+}
+
+// 16 NT rows of w against all of x (up to 16 MT rows) per workgroup.  Its NW
+// waves deal the 128-byte units of the rows among themselves; every lane reads
+// its chunks of w and x straight into the operands of the matrix cores, U
+// units in flight at a time.
+template <typename T, int MT, int NT, int NW, int U>
+__global__ __launch_bounds__(64 * NW) void linear_rows(LinearArgs a) {
+    constexpr int C = Vec<T>::chunk, UNIT = 8 * C;
+    __shared__ __align__(16) f32x4 red[NW * NT * MT * 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int n0 = blockIdx.x * 16 * NT, r = lane & 15, g = lane >> 4;
+    // Rows past the end repeat the last one; their results are not stored.
+    const T *w[NT], *x[MT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) w[i] = (const T*)a.w + (int64_t)min(n0 + 16 * i + r, a.n - 1) * a.k + g * C;
+#pragma unroll
+    for (int j = 0; j < MT; ++j) x[j] = (const T*)a.x + (int64_t)min(16 * j + r, a.m - 1) * a.xs + g * C;
+    f32x4 acc[NT][MT] = {};
+    for (int k0 = wave * UNIT; k0 < a.k; k0 += NW * U * UNIT) {
+        u32x4 fw[U][2][NT], fx[U][2][MT];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = k0 + u * NW * UNIT + h * 4 * C, left = a.k - k - g * C;   // elements from this lane's first
+#pragma unroll
+                for (int i = 0; i < NT; ++i) fw[u][h][i] = load_chunk<T>(w[i] + k, left);
+#pragma unroll
+                for (int j = 0; j < MT; ++j) fx[u][h][j] = load_chunk<T>(x[j] + k, left);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int j = 0; j < MT; ++j) acc[i][j] = mfma_step<T>(fw[u][h][i], fx[u][h][j], acc[i][j]);
+    }
+    rows_store<T, MT, NT, NW>(a, acc, red, n0, wave, lane);
+}
+
+// The same through LDS: every wave has a ring of S stages of its own, each one
+// unit of all rows, and copies S - 1 units ahead of its products; the copies
+// move whole 128-byte lines, where the operands' layout makes register loads
+// take 64 bytes of 16 rows at a time.
+template <typename T, int MT, int NT, int NW, int S>
+__global__ __launch_bounds__(64 * NW) void linear_rows_ring(LinearArgs a) {
+    constexpr int C = Vec<T>::chunk, UNIT = 8 * C, ROWS = 16 * (NT + MT), LD = ROWS / 8;
+    constexpr int RING = NW * S * ROWS * 8, RED = NW * NT * MT * 64;
+    __shared__ __align__(16) u32x4 lds[RING > RED ? RING : RED];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n0 = blockIdx.x * 16 * NT, r = lane & 15, g = lane >> 4;
+    u32x4* ring = lds + wave * S * ROWS * 8;
+    // Copy i takes rows 8 i .. 8 i + 7 of the stage: first w's, then x's.
+    // Chunk c of row i is stored at c ^ (i / 2 % 8).
+    const int lr = lane >> 3;
+    uint32_t off[LD];
+    int lc[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) lc[i] = (lane & 7) ^ (((8 * i + lr) >> 1) & 7);
+#pragma unroll
+    for (int i = 0; i < LD; ++i) {
+        const int row = 8 * i + lr;
+        const int64_t el = i < 2 * NT ? (int64_t)(min(n0 + row, a.n - 1) - n0) * a.k
+                                      : min(row - 16 * NT, a.m - 1) * a.xs;
+        off[i] = (uint32_t)((el + lc[i & 1] * C) * (int)sizeof(T));
+    }
+    const T *wb = (const T*)a.w + (int64_t)n0 * a.k, *xb = (const T*)a.x;
+    // A chunk past k is copied from the unit's start, and zeros are written over it.
+    const auto copy = [&](int k0, int stage) {
+        if (k0 >= a.k) return;
+#pragma unroll
+        for (int i = 0; i < LD; ++i) {
+            const uint32_t back = k0 + lc[i & 1] * C < a.k ? 0 : lc[i & 1] * 16;
+            copy16_to_lds((i < 2 * NT ? wb : xb) + k0, off[i] - back, ring + stage * ROWS * 8 + i * 64);
+        }
+    };
+    f32x4 acc[NT][MT] = {};
+#pragma unroll
+    for (int j = 0; j < S - 1; ++j) copy((wave + j * NW) * UNIT, j);
+    int stage = 0;
+    for (int k0 = wave * UNIT; k0 < a.k; k0 += NW * UNIT) {
+        copy(k0 + (S - 1) * NW * UNIT, stage == 0 ? S - 1 : stage - 1);
+        if (k0 + (S - 1) * NW * UNIT < a.k)
+            wait_vmem<(S - 1) * LD>();
+        else
+            wait_vmem<0>();
+        u32x4* st = ring + stage * ROWS * 8;
+        if (k0 + UNIT > a.k) {
+#pragma unroll
+            for (int i = 0; i < LD; ++i)
+                if (k0 + lc[i & 1] * C >= a.k) st[i * 64 + lane] = u32x4{0, 0, 0, 0};
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        u32x4 fw[2][NT], fx[2][MT];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = (4 * h + g) ^ ((r >> 1) & 7);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) fw[h][i] = st[(16 * i + r) * 8 + c];
+#pragma unroll
+            for (int j = 0; j < MT; ++j) fx[h][j] = st[(16 * (NT + j) + r) * 8 + c];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int j = 0; j < MT; ++j) acc[i][j] = mfma_step<T>(fw[h][i], fx[h][j], acc[i][j]);
+        // The stage's reads have returned before it is copied to again.
+        __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0)
+        stage = stage == S - 1 ? 0 : stage + 1;
+    }
+    __syncthreads();
+    rows_store<T, MT, NT, NW>(a, acc, (f32x4*)lds, n0, wave, lane);
+}
+
+template <typename T, int MT, int NT, int NW, int U>
+hipError_t run(const LinearArgs& a, hipStream_t s) {
+    const dim3 grid((uint32_t)((a.n + 16 * NT - 1) / (16 * NT))), block(64 * NW);
+    linear_rows<T, MT, NT, NW, U><<<grid, block, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T, int MT, int NT, int NW, int S>
+hipError_t run_ring(const LinearArgs& a, hipStream_t s) {
+    linear_rows_ring<T, MT, NT, NW, S><<<dim3((uint32_t)((a.n + 16 * NT - 1) / (16 * NT))), dim3(64 * NW), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t run(const LinearArgs& a, hipStream_t s) {
+    if (a.vec) {
+        // Waves, stages: the fastest of those tried at 1 to 128 rows, among
+        // them 16 waves, 2 to 8 stages and 32 or 64 rows of w a workgroup.
+        if (a.m <= 16) return run_ring<T, 1, 1, 8, 2>(a, s);
+        if (a.m <= 32) return run_ring<T, 2, 1, 4, 3>(a, s);
+        if (a.m <= 64) return run_ring<T, 4, 1, 4, 2>(a, s);
+        return run_ring<T, 8, 1, 4, 2>(a, s);
+    }
+    if (a.m <= 16) return run<T, 1, 1, 8, 4>(a, s);
+    return run<T, 2, 1, 8, 2>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_linear_rows(int32_t dtype, const LinearArgs& a, hipStream_t s) {
+    return dtype == CONV_DTYPE_F32 ? run<float>(a, s) : run<bf16>(a, s);
+}
+
+}  // namespace conv2d

@@ -29,14 +29,14 @@ __device__ __forceinline__ void turn_sincos(double t, float* s, float* c) {
 }
 
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int64_t off0, int64_t off1, f32x4& a, f32x4& b) {
+__device__ __forceinline__ void load44(const T* p, int64_t off0, int64_t off1, f32x4& a, f32x4& b) {
     typedef typename Vec<T>::v4 V;
     a = to_f32(*(const V*)(p + off0));
     b = to_f32(*(const V*)(p + off1));
 }
 
 template <typename T>
-__device__ __forceinline__ void store8(T* p, int64_t off0, int64_t off1, f32x4 a, f32x4 b) {
+__device__ __forceinline__ void store44(T* p, int64_t off0, int64_t off1, f32x4 a, f32x4 b) {
     typedef typename Vec<T>::v4 V;
     *(V*)(p + off0) = from_f32<T>(a);
     *(V*)(p + off1) = from_f32<T>(b);
@@ -93,7 +93,7 @@ __global__ __launch_bounds__(256) void qk_rope_vec(RopeArgs a, int parts, DivU32
         const int h = h0 + lane / LPH;
         const bool on = live && h < heads;
         f32x4 x0{0, 0, 0, 0}, x1{0, 0, 0, 0};
-        if (on) load8(in + (int64_t)h * a.d, o0, o1, x0, x1);
+        if (on) load44(in + (int64_t)h * a.d, o0, o1, x0, x1);
         const bool is_q = h < a.heads_q, is_v = h >= a.heads_q + a.heads_kv;
         if (norm) {
             float ss = 0;
@@ -126,11 +126,11 @@ __global__ __launch_bounds__(256) void qk_rope_vec(RopeArgs a, int parts, DivU32
         }
         if (!on) continue;
         if (is_q)
-            store8(qo + (int64_t)h * a.d, o0, o1, x0, x1);
+            store44(qo + (int64_t)h * a.d, o0, o1, x0, x1);
         else if (keep && !is_v)
-            store8(ko + (int64_t)(h - a.heads_q) * a.d, o0, o1, x0, x1);
+            store44(ko + (int64_t)(h - a.heads_q) * a.d, o0, o1, x0, x1);
         else if (keep)
-            store8(vo + (int64_t)(h - a.heads_q - a.heads_kv) * a.d, o0, o1, x0, x1);
+            store44(vo + (int64_t)(h - a.heads_q - a.heads_kv) * a.d, o0, o1, x0, x1);
     }
 }
 

@@ -48,4 +48,38 @@ __device__ __forceinline__ typename Vec<T>::v4 from_f32(f32x4 v) {
     return __builtin_convertvector(v, typename Vec<T>::v4);
 }
 
+// Eight elements at a 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ f32x8 load8(const T* p) {
+    typedef T V __attribute__((ext_vector_type(8)));
+    return __builtin_convertvector(*(const V*)p, f32x8);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, f32x8 v) {
+    typedef T V __attribute__((ext_vector_type(8)));
+    *(V*)p = __builtin_convertvector(v, V);
+}
+
+// 16 bytes per lane from base + off (bytes) straight to LDS: lane l writes
+// lds + 16 l (lds wave-uniform).  Inline assembly, so that the compiler does
+// not order later LDS reads of the other stage behind it; the kernels' own
+// waits order the copies.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void copy16_to_lds(const void* base, uint32_t off, const u32x4* lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const uint32_t m = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(m)
+                 : "memory", "m0");
+#endif
+}
+#pragma clang diagnostic pop
+
+// Waits until at most N of this thread's vector memory operations are left.
+template <int N>
+__device__ __forceinline__ void wait_vmem() {
+    static_assert(N < 64, "counter");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+
 }  // namespace conv2d
