@@ -294,7 +294,11 @@ hipError_t launch_attention_join(int32_t dtype, const AttnArgs& a, hipStream_t s
 
 AttnPlan plan_attention(int32_t dtype, const AttnArgs& a) {
     AttnPlan p{};
-    p.row_tiles = (a.rows + 63) / 64;
+    // 64 keys within 32-bit byte offsets.
+    const bool near = a.k_s[1] < 1 << 25 && a.v_s[1] < 1 << 25;
+    p.kernel = dtype == CONV_DTYPE_BF16 && a.rows > 32 && near ? ATTN_TILE : ATTN_ANY;
+    const int tile = p.kernel == ATTN_TILE ? 128 : 64;
+    p.row_tiles = (a.rows + tile - 1) / tile;
     p.splits = 1;
     // Few row tiles leave compute units without work: the keys are then split
     // so that about two workgroups a unit run, each over 256 keys at least.
@@ -310,7 +314,9 @@ AttnPlan plan_attention(int32_t dtype, const AttnArgs& a) {
 }
 
 hipError_t launch_attention(int32_t dtype, const AttnPlan& p, const AttnArgs& a, hipStream_t s) {
-    const hipError_t e = dtype == CONV_DTYPE_F32 ? run_any<float>(a, s) : run_any<bf16>(a, s);
+    const hipError_t e = p.kernel == ATTN_TILE           ? launch_attention_tile(a, s)
+                         : dtype == CONV_DTYPE_F32 ? run_any<float>(a, s)
+                                                   : run_any<bf16>(a, s);
     if (e != hipSuccess || p.splits == 1) return e;
     return launch_attention_join(dtype, a, s);
 }

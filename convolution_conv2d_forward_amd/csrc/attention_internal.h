@@ -74,13 +74,17 @@ struct AttnArgs {
     float softcap;          // 0: none
 };
 
+// Kernels of attention_forward: any type and size, or many rows in bf16.
+enum attn_kernel_t { ATTN_ANY, ATTN_TILE };
+
 // Workgroups and split of the keys that a call of these sizes runs with.
 struct AttnPlan {
-    int32_t kernel;         // attn_kernel_t
+    attn_kernel_t kernel;
     int32_t row_tiles, splits;
     int64_t ws_bytes;
 };
 
+hipError_t launch_attention_tile(const AttnArgs& a, hipStream_t s);
 AttnPlan plan_attention(int32_t dtype, const AttnArgs& a);
 hipError_t launch_attention(int32_t dtype, const AttnPlan& p, const AttnArgs& a, hipStream_t s);
 
