@@ -233,34 +233,65 @@ __global__ __launch_bounds__(256) void attention_any(AttnArgs a) {
     if (g == 0) *ws_stat(a, wr) = f32x2{m_run, l_run};
 }
 
-// One wave per row: the splits' maxima and sums give each split's factor,
-// then every lane adds up its elements over the splits.
-template <typename T>
-__global__ __launch_bounds__(256) void attention_join(AttnArgs a, uint32_t waves) {
-    const uint32_t w = blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (w >= waves) return;
-    const int lane = threadIdx.x & 63;
-    const int bh = (int)(w / (uint32_t)a.rows), row = (int)(w % (uint32_t)a.rows);
+// A workgroup per row.  The splits' maxima and sums give each split's factor;
+// then groups of threads, each as wide as the row, add up the outputs of every
+// GROUPS-th split, four loads in flight, and meet in LDS.
+template <typename T, int DP>
+__global__ __launch_bounds__(256) void attention_join(AttnArgs a) {
+    constexpr int W = DP / 4, GROUPS = 256 / W;
+    __shared__ float top_w[4], sum_w[4], factor[256];
+    __shared__ __align__(16) f32x4 part[GROUPS][W];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int bh = (int)(blockIdx.x / (uint32_t)a.rows), row = (int)(blockIdx.x % (uint32_t)a.rows);
     const int b = bh / a.heads_kv, hk = bh % a.heads_kv;
     const int qi = row / a.group, hq = hk * a.group + row % a.group;
-    float top = -INFINITY;
-    for (int s = lane; s < a.splits; s += 64) top = fmaxf(top, (*ws_stat(a, ws_row(a, bh, s, row)))[0]);
+    const int64_t at = ws_row(a, bh, 0, row);
+    const int grp = tid / W, e = (tid % W) * 4;
+    f32x4 sum{0, 0, 0, 0};
+    f32x2 st{-INFINITY, 0.0f};
+    if (tid < a.splits) st = *ws_stat(a, at + (int64_t)tid * a.rows);
+    // The first outputs are on their way while the factors are formed.
+    f32x4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int s = grp + i * GROUPS;
+        v[i] = f32x4{0, 0, 0, 0};
+        if (s < a.splits && e < a.d) v[i] = *(const f32x4*)(ws_out(a, at + (int64_t)s * a.rows) + e);
+    }
+    float top = st[0];
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m, 64));
-    const float base = top == -INFINITY ? 0.0f : top;
-    f32x4 sum{0, 0, 0, 0};
-    float l = 0.0f;
-    const int e = lane * 4;
-    for (int s = 0; s < a.splits; ++s) {
-        const int64_t wr = ws_row(a, bh, s, row);
-        const f32x2 st = *ws_stat(a, wr);
-        const float f = __builtin_amdgcn_exp2f(st[0] - base);
-        l += f * st[1];
-        if (e < a.d) sum += *(const f32x4*)(ws_out(a, wr) + e) * f;
+    if (lane == 0) top_w[wave] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(top_w[0], top_w[1]), fmaxf(top_w[2], top_w[3]));
+    const float f = __builtin_amdgcn_exp2f(st[0] - (top == -INFINITY ? 0.0f : top));
+    factor[tid] = f;
+    float l = f * st[1];
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) l += __shfl_xor(l, m, 64);
+    if (lane == 0) sum_w[wave] = l;
+    __syncthreads();
+    l = sum_w[0] + sum_w[1] + sum_w[2] + sum_w[3];
+    for (int s0 = grp; s0 < a.splits; s0 += 4 * GROUPS) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s = s0 + i * GROUPS;
+            if (s < a.splits) sum += v[i] * factor[s];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s = s0 + (i + 4) * GROUPS;
+            if (s < a.splits && e < a.d) v[i] = *(const f32x4*)(ws_out(a, at + (int64_t)s * a.rows) + e);
+        }
     }
+    part[grp][tid % W] = sum;
+    __syncthreads();
+    if (grp != 0 || e >= a.d) return;
+#pragma unroll
+    for (int i = 1; i < GROUPS; ++i) sum += part[i][tid];
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     T* op = (T*)a.out + b * a.o_s[0] + qi * a.o_s[1] + hq * a.o_s[2];
-    if (e < a.d) *(typename Vec<T>::v4*)(op + e) = from_f32<T>(sum * inv);
+    *(typename Vec<T>::v4*)(op + e) = from_f32<T>(sum * inv);
 }
 
 template <typename T, int DP>
@@ -281,40 +312,57 @@ hipError_t run_any(const AttnArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_attention_join(int32_t dtype, const AttnArgs& a, hipStream_t s) {
-    const int64_t waves = (int64_t)a.batch * a.heads_kv * a.rows;
-    if (waves > 0xfffffff0ll) return hipErrorInvalidValue;
-    const dim3 grid((uint32_t)((waves + 3) / 4));
-    if (dtype == CONV_DTYPE_F32)
-        attention_join<float><<<grid, dim3(256), 0, s>>>(a, (uint32_t)waves);
+template <typename T>
+static hipError_t run_join(const AttnArgs& a, hipStream_t s) {
+    const dim3 grid((uint32_t)((int64_t)a.batch * a.heads_kv * a.rows)), block(256);
+    if (a.d <= 32)
+        attention_join<T, 32><<<grid, block, 0, s>>>(a);
+    else if (a.d <= 64)
+        attention_join<T, 64><<<grid, block, 0, s>>>(a);
+    else if (a.d <= 128)
+        attention_join<T, 128><<<grid, block, 0, s>>>(a);
     else
-        attention_join<bf16><<<grid, dim3(256), 0, s>>>(a, (uint32_t)waves);
+        attention_join<T, 256><<<grid, block, 0, s>>>(a);
     return hipGetLastError();
+}
+
+hipError_t launch_attention_join(int32_t dtype, const AttnArgs& a, hipStream_t s) {
+    return dtype == CONV_DTYPE_F32 ? run_join<float>(a, s) : run_join<bf16>(a, s);
 }
 
 AttnPlan plan_attention(int32_t dtype, const AttnArgs& a) {
     AttnPlan p{};
     // 64 keys within 32-bit byte offsets.
     const bool near = a.k_s[1] < 1 << 25 && a.v_s[1] < 1 << 25;
-    p.kernel = dtype == CONV_DTYPE_BF16 && a.rows > 32 && near ? ATTN_TILE : ATTN_ANY;
-    const int tile = p.kernel == ATTN_TILE ? 128 : 64;
+    // 17 to 32 rows in bf16, 32 rows of 128 over 8x4096 keys: 39.5 us in one
+    // tile, 48.6 in two of 16 rows.
+    p.kernel = a.rows <= (dtype == CONV_DTYPE_F32 ? 32 : 16)       ? ATTN_ROWS
+               : dtype == CONV_DTYPE_BF16 && near ? ATTN_TILE
+                                                  : ATTN_ANY;
+    const int tile = p.kernel == ATTN_ROWS ? 16 : p.kernel == ATTN_TILE ? 128 : 64;
     p.row_tiles = (a.rows + tile - 1) / tile;
-    p.splits = 1;
-    // Few row tiles leave compute units without work: the keys are then split
-    // so that about two workgroups a unit run, each over 256 keys at least.
-    const int64_t tiles = (int64_t)a.batch * a.heads_kv * p.row_tiles, want = 2 * (int64_t)device_cu_count();
-    if (tiles < want) {
-        int64_t s = (want + tiles - 1) / tiles;
-        const int64_t most = ((int64_t)a.kv_len + 255) / 256;
-        if (s > most) s = most;
-        p.splits = s < 1 ? 1 : (int32_t)s;
+    // Few row tiles leave compute units without work: the keys are then split.
+    const int64_t tiles = (int64_t)a.batch * a.heads_kv * p.row_tiles, cus = device_cu_count();
+    int64_t want = 2 * cus, keys = 256;   // workgroups, and keys for each at least
+    if (p.kernel == ATTN_ROWS) {
+        // Two workgroups fit on a unit (one where a row of K has more than 256
+        // bytes); a third per unit evens out sequences of different lengths.
+        const bool big = a.d * (dtype == CONV_DTYPE_F32 ? 4 : 2) > 256;
+        want = big ? cus : a.batch > 1 ? 3 * cus : 2 * cus;
+        keys = tiles >= cus ? 1024 : tiles * 2 >= cus ? 512 : 128;
     }
+    int64_t s = tiles < want ? (want + tiles - 1) / tiles : 1;
+    const int64_t most = ((int64_t)a.kv_len + keys - 1) / keys;
+    if (s > most) s = most;
+    if (s > ATTN_MAX_SPLITS) s = ATTN_MAX_SPLITS;
+    p.splits = s < 1 ? 1 : (int32_t)s;
     if (p.splits > 1) p.ws_bytes = (int64_t)a.batch * a.heads_kv * p.splits * a.rows * (a.d + 2) * 4;
     return p;
 }
 
 hipError_t launch_attention(int32_t dtype, const AttnPlan& p, const AttnArgs& a, hipStream_t s) {
-    const hipError_t e = p.kernel == ATTN_TILE           ? launch_attention_tile(a, s)
+    const hipError_t e = p.kernel == ATTN_ROWS        ? launch_attention_rows(dtype, a, s)
+                         : p.kernel == ATTN_TILE      ? launch_attention_tile(a, s)
                          : dtype == CONV_DTYPE_F32 ? run_any<float>(a, s)
                                                    : run_any<bf16>(a, s);
     if (e != hipSuccess || p.splits == 1) return e;

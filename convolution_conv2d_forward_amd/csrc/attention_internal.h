@@ -74,8 +74,11 @@ struct AttnArgs {
     float softcap;          // 0: none
 };
 
-// Kernels of attention_forward: any type and size, or many rows in bf16.
-enum attn_kernel_t { ATTN_ANY, ATTN_TILE };
+// Kernels of attention_forward: any type and size, up to 16 rows for each key
+// head, or many rows in bf16.
+enum attn_kernel_t { ATTN_ANY, ATTN_ROWS, ATTN_TILE };
+
+constexpr int ATTN_MAX_SPLITS = 256;   // a join workgroup takes one a thread
 
 // Workgroups and split of the keys that a call of these sizes runs with.
 struct AttnPlan {
@@ -84,6 +87,7 @@ struct AttnPlan {
     int64_t ws_bytes;
 };
 
+hipError_t launch_attention_rows(int32_t dtype, const AttnArgs& a, hipStream_t s);
 hipError_t launch_attention_tile(const AttnArgs& a, hipStream_t s);
 AttnPlan plan_attention(int32_t dtype, const AttnArgs& a);
 hipError_t launch_attention(int32_t dtype, const AttnPlan& p, const AttnArgs& a, hipStream_t s);
