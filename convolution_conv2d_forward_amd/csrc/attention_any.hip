@@ -47,7 +47,7 @@ __global__ __launch_bounds__(256) void attention_any(AttnArgs a) {
     const bool live = row < a.rows;
     const int qi = live ? row / a.group : 0, hq = hk * a.group + (live ? row - qi * a.group : 0);
     int lo = 0, hi = 0;
-    if (live) row_interval(a, sl, b, qi, lo, hi);
+    row_interval(a, sl, b, qi, live, lo, hi);
     const bool empty = hi <= lo;
     int min_lo = empty ? INT32_MAX : lo, max_hi = hi;
     // Rows past the end do not count against a tile being seen whole.
@@ -233,6 +233,48 @@ __global__ __launch_bounds__(256) void attention_any(AttnArgs a) {
     if (g == 0) *ws_stat(a, wr) = f32x2{m_run, l_run};
 }
 
+// Few splits: as many threads as the row is wide add up its outputs.
+template <typename T, int DP>
+__global__ __launch_bounds__(256) void attention_join_few(AttnArgs a, uint32_t all_rows) {
+    constexpr int W = DP / 4;
+    const uint32_t at_row = blockIdx.x * (256 / W) + threadIdx.x / W;
+    const int e = (threadIdx.x % W) * 4;
+    if (at_row >= all_rows || e >= a.d) return;
+    const int bh = (int)(at_row / (uint32_t)a.rows), row = (int)(at_row % (uint32_t)a.rows);
+    const int b = bh / a.heads_kv, hk = bh % a.heads_kv;
+    const int qi = row / a.group, hq = hk * a.group + row % a.group;
+    const int64_t at = ws_row(a, bh, 0, row);
+    float top = -INFINITY, l = 0.0f;
+    f32x4 sum{0, 0, 0, 0};
+    for (int s0 = 0; s0 < a.splits; s0 += 4) {
+        f32x2 st[4];
+        f32x4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t wr = at + (int64_t)min(s0 + i, a.splits - 1) * a.rows;
+            st[i] = *ws_stat(a, wr);
+            v[i] = *(const f32x4*)(ws_out(a, wr) + e);
+            if (s0 + i >= a.splits) st[i] = f32x2{-INFINITY, 0.0f};
+        }
+        float m = top;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = fmaxf(m, st[i][0]);
+        const float base = m == -INFINITY ? 0.0f : m, fade = __builtin_amdgcn_exp2f(top - base);
+        top = m;
+        l *= fade;
+        sum *= fade;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float f = __builtin_amdgcn_exp2f(st[i][0] - base);
+            l += f * st[i][1];
+            if (s0 + i < a.splits) sum += v[i] * f;
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    T* op = (T*)a.out + b * a.o_s[0] + qi * a.o_s[1] + hq * a.o_s[2];
+    *(typename Vec<T>::v4*)(op + e) = from_f32<T>(sum * inv);
+}
+
 // A workgroup per row.  The splits' maxima and sums give each split's factor;
 // then groups of threads, each as wide as the row, add up the outputs of every
 // GROUPS-th split, four loads in flight, and meet in LDS.
@@ -312,18 +354,25 @@ hipError_t run_any(const AttnArgs& a, hipStream_t s) {
 
 }  // namespace
 
+template <typename T, int DP>
+static hipError_t run_join(const AttnArgs& a, hipStream_t s) {
+    const int64_t rows = (int64_t)a.batch * a.heads_kv * a.rows;
+    // 517 rows x 24 heads in 3 splits: 4 us by 8 rows a workgroup, 12 by one.
+    if (a.splits <= 8) {
+        constexpr int R = 256 / (DP / 4);
+        attention_join_few<T, DP><<<dim3((uint32_t)((rows + R - 1) / R)), dim3(256), 0, s>>>(a, (uint32_t)rows);
+    } else {
+        attention_join<T, DP><<<dim3((uint32_t)rows), dim3(256), 0, s>>>(a);
+    }
+    return hipGetLastError();
+}
+
 template <typename T>
 static hipError_t run_join(const AttnArgs& a, hipStream_t s) {
-    const dim3 grid((uint32_t)((int64_t)a.batch * a.heads_kv * a.rows)), block(256);
-    if (a.d <= 32)
-        attention_join<T, 32><<<grid, block, 0, s>>>(a);
-    else if (a.d <= 64)
-        attention_join<T, 64><<<grid, block, 0, s>>>(a);
-    else if (a.d <= 128)
-        attention_join<T, 128><<<grid, block, 0, s>>>(a);
-    else
-        attention_join<T, 256><<<grid, block, 0, s>>>(a);
-    return hipGetLastError();
+    if (a.d <= 32) return run_join<T, 32>(a, s);
+    if (a.d <= 64) return run_join<T, 64>(a, s);
+    if (a.d <= 128) return run_join<T, 128>(a, s);
+    return run_join<T, 256>(a, s);
 }
 
 hipError_t launch_attention_join(int32_t dtype, const AttnArgs& a, hipStream_t s) {
@@ -332,18 +381,21 @@ hipError_t launch_attention_join(int32_t dtype, const AttnArgs& a, hipStream_t s
 
 AttnPlan plan_attention(int32_t dtype, const AttnArgs& a) {
     AttnPlan p{};
-    // 64 keys within 32-bit byte offsets.
-    const bool near = a.k_s[1] < 1 << 25 && a.v_s[1] < 1 << 25;
+    // A tile's keys within 32-bit byte offsets.
+    const bool near = a.k_s[1] < 1 << 24 && a.v_s[1] < 1 << 24;
     // 17 to 32 rows in bf16, 32 rows of 128 over 8x4096 keys: 39.5 us in one
     // tile, 48.6 in two of 16 rows.
     p.kernel = a.rows <= (dtype == CONV_DTYPE_F32 ? 32 : 16)       ? ATTN_ROWS
-               : dtype == CONV_DTYPE_BF16 && near ? ATTN_TILE
-                                                  : ATTN_ANY;
-    const int tile = p.kernel == ATTN_ROWS ? 16 : p.kernel == ATTN_TILE ? 128 : 64;
+               : near ? ATTN_TILE_128
+                      : ATTN_ANY;
+    if (p.kernel == ATTN_TILE_128 && !(dtype == CONV_DTYPE_F32 && a.d > 128) &&
+        (int64_t)a.batch * a.heads_kv * ((a.rows + 127) / 128) < 2 * device_cu_count())
+        p.kernel = ATTN_TILE_64;
+    const int tile = p.kernel == ATTN_ROWS ? 16 : p.kernel == ATTN_TILE_128 ? 128 : 64;
     p.row_tiles = (a.rows + tile - 1) / tile;
     // Few row tiles leave compute units without work: the keys are then split.
     const int64_t tiles = (int64_t)a.batch * a.heads_kv * p.row_tiles, cus = device_cu_count();
-    int64_t want = 2 * cus, keys = 256;   // workgroups, and keys for each at least
+    int64_t want = p.kernel == ATTN_TILE_64 ? cus : 2 * cus, keys = 256;   // workgroups, and keys for each at least
     if (p.kernel == ATTN_ROWS) {
         // Two workgroups fit on a unit (one where a row of K has more than 256
         // bytes); a third per unit evens out sequences of different lengths.
@@ -361,10 +413,15 @@ AttnPlan plan_attention(int32_t dtype, const AttnArgs& a) {
 }
 
 hipError_t launch_attention(int32_t dtype, const AttnPlan& p, const AttnArgs& a, hipStream_t s) {
-    const hipError_t e = p.kernel == ATTN_ROWS        ? launch_attention_rows(dtype, a, s)
-                         : p.kernel == ATTN_TILE      ? launch_attention_tile(a, s)
-                         : dtype == CONV_DTYPE_F32 ? run_any<float>(a, s)
-                                                   : run_any<bf16>(a, s);
+    const bool f32 = dtype == CONV_DTYPE_F32;
+    const int rows = p.kernel == ATTN_TILE_128 ? 128 : 64;
+    hipError_t e;
+    if (p.kernel == ATTN_ROWS)
+        e = launch_attention_rows(dtype, a, s);
+    else if (p.kernel == ATTN_ANY)
+        e = f32 ? run_any<float>(a, s) : run_any<bf16>(a, s);
+    else
+        e = f32 ? launch_attention_tile<float>(a, rows, s) : launch_attention_tile<bf16>(a, rows, s);
     if (e != hipSuccess || p.splits == 1) return e;
     return launch_attention_join(dtype, a, s);
 }

@@ -22,12 +22,13 @@ __device__ __forceinline__ SeqLens seq_lens(const AttnArgs& a, int b) {
     return s;
 }
 
-// The keys that query i of sequence b sees.  Empty: lo = hi = 0.
-__device__ __forceinline__ void row_interval(const AttnArgs& a, SeqLens s, int b, int i, int& lo, int& hi) {
+// The keys that query i of sequence b sees; for all lanes of a wave at once
+// (`live` false: none).  Empty: lo = hi = 0.
+__device__ __forceinline__ void row_interval(const AttnArgs& a, SeqLens s, int b, int i, bool live, int& lo, int& hi) {
     const int p = s.nk - s.nq + i;
     lo = 0;
     hi = s.nk;
-    if (i >= s.nq) hi = 0;
+    if (!live || i >= s.nq) hi = 0;
     if (a.causal) {
         int end = p + 1;
         if (a.prefix_lens) end = max(end, a.prefix_lens[b]);
@@ -38,23 +39,34 @@ __device__ __forceinline__ void row_interval(const AttnArgs& a, SeqLens s, int b
         hi = (int)min((int64_t)hi, (int64_t)p + a.window);
     }
     if (a.doc_offsets) {
-        // The last document that starts at or before p: the number of
-        // borders <= p, by halving.  Offsets that do not ascend select some
-        // document; the interval stays within the sequence.
+        // n: the number of borders <= p, so that document n - 1 holds p.
+        // Offsets that do not ascend select some document; the interval stays
+        // within the sequence.
         const int32_t* o = a.doc_offsets + (int64_t)b * (a.n_docs + 1);
-        int n0 = 0, n1 = a.n_docs + 1;
-        while (n0 < n1) {
-            const int mid = (n0 + n1) >> 1;
-            if (o[mid] <= p)
-                n0 = mid + 1;
-            else
-                n1 = mid;
+        int n = 0, from = 0, to = 0;
+        if (a.n_docs < 64) {
+            // One load, a border a lane, and no chain of loads.
+            const int lane = threadIdx.x & 63, mine = o[min(lane, a.n_docs)];
+            for (int j = 0; j <= a.n_docs; ++j) n += __builtin_amdgcn_readlane(mine, j) <= p;
+            from = __shfl(mine, max(n - 1, 0), 64);
+            to = __shfl(mine, min(n, a.n_docs), 64);
+        } else {
+            int n1 = a.n_docs + 1;
+            while (n < n1) {
+                const int mid = (n + n1) >> 1;
+                if (o[mid] <= p)
+                    n = mid + 1;
+                else
+                    n1 = mid;
+            }
+            from = o[max(n - 1, 0)];
+            to = o[min(n, a.n_docs)];
         }
-        if (n0 == 0 || n0 > a.n_docs || p < 0) {
+        if (n == 0 || n > a.n_docs || p < 0) {
             hi = 0;
         } else {
-            lo = max(lo, o[n0 - 1]);
-            hi = min(hi, o[n0]);
+            lo = max(lo, from);
+            hi = min(hi, to);
         }
     }
     if (hi <= lo) lo = hi = 0;
@@ -130,6 +142,14 @@ __device__ __forceinline__ f32x2* ws_stat(const AttnArgs& a, int64_t row) {
     const int64_t all = (int64_t)a.batch * a.heads_kv * a.splits * a.rows;
     return (f32x2*)(a.ws + all * a.d) + row;
 }
+
+// Tiles of 128 or 64 rows (attention_tile.h).
+template <typename T>
+hipError_t launch_attention_tile(const AttnArgs& a, int rows, hipStream_t s);
+template <>
+hipError_t launch_attention_tile<float>(const AttnArgs& a, int rows, hipStream_t s);
+template <>
+hipError_t launch_attention_tile<bf16>(const AttnArgs& a, int rows, hipStream_t s);
 
 // Joins the splits' results (attention_any.hip).
 hipError_t launch_attention_join(int32_t dtype, const AttnArgs& a, hipStream_t s);

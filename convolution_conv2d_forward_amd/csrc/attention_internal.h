@@ -74,9 +74,9 @@ struct AttnArgs {
     float softcap;          // 0: none
 };
 
-// Kernels of attention_forward: any type and size, up to 16 rows for each key
-// head, or many rows in bf16.
-enum attn_kernel_t { ATTN_ANY, ATTN_ROWS, ATTN_TILE };
+// Kernels of attention_forward: any strides, few rows for each key head, or
+// many.
+enum attn_kernel_t { ATTN_ANY, ATTN_ROWS, ATTN_TILE_128, ATTN_TILE_64 };
 
 constexpr int ATTN_MAX_SPLITS = 256;   // a join workgroup takes one a thread
 
@@ -88,7 +88,6 @@ struct AttnPlan {
 };
 
 hipError_t launch_attention_rows(int32_t dtype, const AttnArgs& a, hipStream_t s);
-hipError_t launch_attention_tile(const AttnArgs& a, hipStream_t s);
 AttnPlan plan_attention(int32_t dtype, const AttnArgs& a);
 hipError_t launch_attention(int32_t dtype, const AttnPlan& p, const AttnArgs& a, hipStream_t s);
 

@@ -99,7 +99,7 @@ __global__ __launch_bounds__((64 * RowsAttn<T, DP>::NW), (RowsAttn<T, DP>::OCC))
     const bool live = row < a.rows;
     const int qi = live ? row / a.group : 0, hq = hk * a.group + (live ? row - qi * a.group : 0);
     int lo = 0, hi = 0;
-    if (live) row_interval(a, sl, b, qi, lo, hi);
+    row_interval(a, sl, b, qi, live, lo, hi);
     const bool empty = hi <= lo;
     int w_lo = empty ? INT32_MAX : lo, w_hi = hi;                                    // keys that some row sees
     int f_lo = live ? (empty ? INT32_MAX : lo) : 0, f_hi = live ? hi : INT32_MAX;    // keys that every row sees

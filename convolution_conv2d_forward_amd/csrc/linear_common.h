@@ -1,5 +1,5 @@
-// Shared by the kernels of linear_forward: matrix-core steps for both types,
-// and the epilogue.
+// Matrix-core steps for both types, and what the kernels of linear_forward
+// share.
 #pragma once
 
 #include <type_traits>
@@ -27,6 +27,24 @@ __device__ __forceinline__ f32x4 mfma_step<float>(u32x4 a, u32x4 b, f32x4 c) {
     const f32x4 fa = __builtin_bit_cast(f32x4, a), fb = __builtin_bit_cast(f32x4, b);
 #pragma unroll
     for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[j], fb[j], c, 0, 0, 0);
+    return c;
+}
+
+// One 32x32 product step over 32 bytes of each row: lane l holds 16 bytes of
+// row (l & 31) of each operand, chunk l >> 5 of the two.  Result: lane l holds
+// rows 8 (i / 4) + 4 (l >> 5) + i % 4 of A against row (l & 31) of B.
+template <typename T>
+__device__ __forceinline__ f32x16 mfma32_step(u32x4 a, u32x4 b, f32x16 c);
+template <>
+__device__ __forceinline__ f32x16 mfma32_step<bf16>(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+template <>
+__device__ __forceinline__ f32x16 mfma32_step<float>(u32x4 a, u32x4 b, f32x16 c) {
+    const f32x4 fa = __builtin_bit_cast(f32x4, a), fb = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[j], fb[j], c, 0, 0, 0);
     return c;
 }
 

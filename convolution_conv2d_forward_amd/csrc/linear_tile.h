@@ -9,24 +9,6 @@ namespace conv2d {
 
 namespace {
 
-// One 32x32 product step over 32 bytes of each row: lane l holds 16 bytes of
-// row (l & 31) of each operand, chunk l >> 5 of the two.  Result: lane l holds
-// rows 8 (i / 4) + 4 (l >> 5) + i % 4 of A against row (l & 31) of B.
-template <typename T>
-__device__ __forceinline__ f32x16 mfma32_step(u32x4 a, u32x4 b, f32x16 c);
-template <>
-__device__ __forceinline__ f32x16 mfma32_step<bf16>(u32x4 a, u32x4 b, f32x16 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
-                                                   0, 0);
-}
-template <>
-__device__ __forceinline__ f32x16 mfma32_step<float>(u32x4 a, u32x4 b, f32x16 c) {
-    const f32x4 fa = __builtin_bit_cast(f32x4, a), fb = __builtin_bit_cast(f32x4, b);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[j], fb[j], c, 0, 0, 0);
-    return c;
-}
-
 // Shape of a tile: BM rows of x by BN rows of w, WM * WN waves, CPR chunks of
 // 16 bytes of every row a step, S stages of LDS.
 template <typename T, int BM_, int BN_, int WM_, int WN_, int CPR_, int S_>
