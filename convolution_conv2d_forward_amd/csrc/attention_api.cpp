@@ -339,7 +339,7 @@ conv_status_t qk_rope_forward(qk_rope_desc_t d, int64_t tokens, const void* qkv,
     a.cache_rows = krows;
     a.tokens = (int32_t)tokens; a.heads_q = p.heads_q; a.heads_kv = p.heads_kv;
     a.d = p.head_dim; a.r = p.rotary_dim; a.eps = p.eps; a.attn_factor = (float)p.attn_factor;
-    memcpy(a.turns, d->turns, sizeof(a.turns));
+    a.turns = d->turns;
     const int64_t chunk = 16 / es;
     const bool vec = aligned16(qkv) && aligned16(q) && aligned16(k) && aligned16(v) &&
                      (!p.has_norm || (aligned16(q_gamma) && aligned16(k_gamma))) && p.head_dim % 8 == 0 &&

@@ -46,7 +46,7 @@ struct RopeArgs {
     int32_t tokens, heads_q, heads_kv, d, r;
     float eps;
     float attn_factor;
-    double turns[ROPE_MAX_PAIRS];   // turns (angle / 2 pi) a position of each pair
+    const double* turns;    // host: ROPE_MAX_PAIRS turns (angle / 2 pi) a position; the launch passes those in use by value
 };
 
 // vec: every row and head starts at a 16-byte boundary.

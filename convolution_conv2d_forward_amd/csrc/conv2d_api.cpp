@@ -53,12 +53,21 @@ conv_status_t conv2d::hip_status(hipError_t e, const char* what) {
 }
 
 // Do two strided views overlap?  Both are lists of n equal-length blocks at a
-// constant stride; walk them in address order (two pointers, O(n1 + n2)).
+// constant stride: equal strides have a closed form, others are walked in
+// address order (two pointers, O(n1 + n2)).
 bool conv2d::views_overlap(const View& a, const View& b) {
     if (a.len == 0 || b.len == 0 || a.n == 0 || b.n == 0) return false;
     const uintptr_t a_end = a.base + (uintptr_t)((a.n - 1) * a.stride + a.len);
     const uintptr_t b_end = b.base + (uintptr_t)((b.n - 1) * b.stride + b.len);
     if (a_end <= b.base || b_end <= a.base) return false;
+    if (a.stride == b.stride && a.stride > 0) {
+        // Block i of a is k = i - j strides from block j of b's origin: the
+        // last such block that starts before b's block ends decides.
+        const int64_t d = (int64_t)(b.base - a.base), s = a.stride, end = d + b.len - 1;
+        int64_t k = end >= 0 ? end / s : -((-end + s - 1) / s);
+        if (k > a.n - 1) k = a.n - 1;
+        return k >= -(b.n - 1) && k * s + a.len > d;
+    }
     int64_t i = 0, j = 0;
     while (i < a.n && j < b.n) {
         const uintptr_t as = a.base + (uintptr_t)(i * a.stride), ae = as + (uintptr_t)a.len;

@@ -28,6 +28,20 @@ __device__ __forceinline__ void turn_sincos(double t, float* s, float* c) {
     sincospif(2.0f * f, s, c);
 }
 
+// The turns of P pairs as a kernel argument: half of a kilobyte less of them is
+// half a microsecond less on the host.
+template <int P>
+struct RopeTurns {
+    double t[P];
+};
+
+template <int P>
+RopeTurns<P> turns_of(const RopeArgs& a) {
+    RopeTurns<P> r;
+    for (int i = 0; i < P; ++i) r.t[i] = a.turns[i];
+    return r;
+}
+
 template <typename T>
 __device__ __forceinline__ void load44(const T* p, int64_t off0, int64_t off1, f32x4& a, f32x4& b) {
     typedef typename Vec<T>::v4 V;
@@ -45,7 +59,8 @@ __device__ __forceinline__ void store44(T* p, int64_t off0, int64_t off1, f32x4 
 // One wave: token blockIdx / parts, heads part, part + parts, ... in steps of
 // the groups of a wave.
 template <typename T, bool HALF, int LPH>
-__global__ __launch_bounds__(256) void qk_rope_vec(RopeArgs a, int parts, DivU32 dv_parts, uint32_t waves) {
+__global__ __launch_bounds__(256) void qk_rope_vec(RopeArgs a, RopeTurns<4 * LPH> turns, int parts, DivU32 dv_parts,
+                                                   uint32_t waves) {
     constexpr int HPW = 64 / LPH;   // heads a wave visits at once
     const uint32_t wave = blockIdx.x * 4 + (threadIdx.x >> 6);
     if (wave >= waves) return;
@@ -68,7 +83,7 @@ __global__ __launch_bounds__(256) void qk_rope_vec(RopeArgs a, int parts, DivU32
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float s, c;
-            turn_sincos(pos * a.turns[unit * 4 + i], &s, &c);
+            turn_sincos(pos * turns.t[unit * 4 + i], &s, &c);
             cs[i] = c * a.attn_factor;
             sn[i] = s * a.attn_factor;
         }
@@ -139,7 +154,8 @@ __global__ __launch_bounds__(256) void qk_rope_vec(RopeArgs a, int parts, DivU32
 // over the row; each thread then reads exactly what it overwrites, so the
 // in-place form holds here too.
 template <typename T, bool HALF>
-__global__ __launch_bounds__(256) void qk_rope_any(RopeArgs a, DivU32 dv_heads, uint32_t waves) {
+__global__ __launch_bounds__(256) void qk_rope_any(RopeArgs a, RopeTurns<ROPE_MAX_PAIRS> turns, DivU32 dv_heads,
+                                                   uint32_t waves) {
     const uint32_t wave = blockIdx.x * 4 + (threadIdx.x >> 6);
     if (wave >= waves) return;
     const int lane = threadIdx.x & 63;
@@ -173,7 +189,7 @@ __global__ __launch_bounds__(256) void qk_rope_any(RopeArgs a, DivU32 dv_heads, 
     for (int i = lane; i < half; i += 64) {
         const int e0 = HALF ? i : 2 * i, e1 = HALF ? i + half : 2 * i + 1;
         float s, c;
-        turn_sincos(pos * a.turns[i], &s, &c);
+        turn_sincos(pos * turns.t[i], &s, &c);
         s *= a.attn_factor;
         c *= a.attn_factor;
         float x0 = to_f32(in[e0]), x1 = to_f32(in[e1]);
@@ -204,7 +220,7 @@ hipError_t run_vec(const RopeArgs& a, hipStream_t s) {
     const int64_t waves = (int64_t)a.tokens * parts;
     if (waves > 0x7fffffff) return hipErrorInvalidValue;
     qk_rope_vec<T, HALF, LPH><<<dim3((uint32_t)((waves + 3) / 4)), dim3(256), 0, s>>>(
-        a, (int)parts, make_divu32((uint32_t)parts), (uint32_t)waves);
+        a, turns_of<4 * LPH>(a), (int)parts, make_divu32((uint32_t)parts), (uint32_t)waves);
     return hipGetLastError();
 }
 
@@ -219,7 +235,7 @@ hipError_t run(bool vec, const RopeArgs& a, hipStream_t s) {
     const int heads = a.heads_q + (a.v ? 2 : 1) * a.heads_kv;
     const int64_t waves = (int64_t)a.tokens * heads;
     if (waves > 0xfffffff0ll) return hipErrorInvalidValue;
-    qk_rope_any<T, HALF><<<dim3((uint32_t)((waves + 3) / 4)), dim3(256), 0, s>>>(a, make_divu32((uint32_t)heads),
+    qk_rope_any<T, HALF><<<dim3((uint32_t)((waves + 3) / 4)), dim3(256), 0, s>>>(a, turns_of<ROPE_MAX_PAIRS>(a), make_divu32((uint32_t)heads),
                                                                                  (uint32_t)waves);
     return hipGetLastError();
 }
