@@ -81,8 +81,12 @@ LinearArgs linear_args(const linear_params_t& p, int64_t rows, const void* x, co
     a.xs = p.x_stride; a.ys = p.y_stride; a.rs = p.residual_stride;
     a.m = (int32_t)rows; a.k = p.k; a.n = p.n;
     a.act = p.act_type; a.act_a = p.act_type == CONV_ACT_RELU ? 0.0f : p.act_params[0]; a.act_b = p.act_params[1];
-    a.vec = p.k % chunk == 0 && p.x_stride % chunk == 0 && aligned16(x) && aligned16(w) &&
-            (p.x_stride > p.k ? p.x_stride : p.k) * es * 256 < (int64_t)1 << 32;
+    if ((p.x_stride > p.k ? p.x_stride : p.k) * es * 256 < (int64_t)1 << 32) {
+        const auto rows_at = [&](int64_t bytes) {
+            return p.k * es % bytes == 0 && p.x_stride * es % bytes == 0 && ((uintptr_t)x | (uintptr_t)w) % bytes == 0;
+        };
+        a.vec = rows_at(16) ? 16 : rows_at(4) ? 4 : 0;
+    }
     const auto out_ok = [&](const void* q, int64_t stride) {
         return stride % chunk == 0 && aligned16(q);
     };

@@ -19,8 +19,8 @@ struct LinearArgs {
     int32_t m, k, n;
     int32_t act;
     float act_a, act_b;
-    int32_t vec;            // x and w rows start at 16-byte boundaries, k fills whole 16-byte chunks, and 256 rows lie
-                            // within 32-bit byte offsets
+    int32_t vec;            // 16 or 4: x and w rows start at boundaries of so many bytes, k fills whole pieces of them,
+                            // and 256 rows lie within 32-bit byte offsets; 0: neither
     int32_t vec_out;        // 8 consecutive outputs of a row start at a 16-byte boundary in y and the residual
 };
 

@@ -18,7 +18,7 @@ namespace {
 // deep ones, 129 in tiles of 64.)
 linear_tile_t pick(int32_t dtype, const LinearArgs& a) {
     if (a.m <= 32) return LINEAR_ROWS;
-    if (a.m <= 128 && a.vec && (int64_t)((a.n + 15) / 16) * ((a.m + 15) / 16 + 1) <= 2304) return LINEAR_ROWS;
+    if (a.m <= 128 && a.vec == 16 && (int64_t)((a.n + 15) / 16) * ((a.m + 15) / 16 + 1) <= 2304) return LINEAR_ROWS;
     const int64_t cus = device_cu_count();
     const auto rounds = [&](int64_t t, int64_t per_cu) {
         const int64_t tiles = ((a.m + t - 1) / t) * ((a.n + t - 1) / t);

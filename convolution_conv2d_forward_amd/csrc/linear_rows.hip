@@ -187,7 +187,7 @@ hipError_t run_ring(const LinearArgs& a, hipStream_t s) {
 
 template <typename T>
 hipError_t run(const LinearArgs& a, hipStream_t s) {
-    if (a.vec) {
+    if (a.vec == 16) {
         // Waves, stages: the fastest of those tried at 1 to 128 rows, among
         // them 16 waves, 2 to 8 stages and 32 or 64 rows of w a workgroup.
         if (a.m <= 16) return run_ring<T, 1, 1, 8, 2>(a, s);

@@ -139,25 +139,30 @@ __device__ __forceinline__ void tile_store(const LinearArgs& a, const f32x16 (&a
     }
 }
 
-// Rows start at 16-byte boundaries and k fills whole chunks: chunks are copied
-// straight to a ring of S LDS stages, S - 1 steps ahead of their use (a copy
-// takes some 1600 cycles to land, more under load).  A workgroup takes one
-// tile after the other, and the copies of the next tile's first steps run
-// through the outputs of the last one: with the tiles in workgroups of their
-// own, all of which end at about the same time, 8192x4096x8192 took 513 us.
-// The operands of product step s + 1 are read while step s multiplies, over
-// the border of two stages too: the barrier that frees a stage stands before
-// the stage's last products, whose operands are in registers by then, so the
+// Chunks are copied straight to a ring of S LDS stages, S - 1 steps ahead of
+// their use (a copy takes some 1600 cycles to land, more under load), in
+// pieces of W bytes: rows start at W-byte boundaries, and k fills whole
+// pieces.  A workgroup takes one tile after the other, and the copies of the
+// next tile's first steps run through the outputs of the last one.  The
+// operands of product step s + 1 are read while step s multiplies, over the
+// border of two stages too: the barrier that frees a stage stands before the
+// stage's last products, whose operands are in registers by then, so the
 // matrix cores have work while the waves meet.
-template <typename T, class C, int ACT>
+template <typename T, class C, int ACT, int W>
 __global__ __launch_bounds__(C::NT, 2) void linear_tile(LinearArgs a, int tiles_m, int tiles_n) {
-    constexpr int S = C::S, LD = C::LD, BK = C::BK, NT = C::NT, CPR = C::CPR, STEPS = CPR / 2;
-    constexpr int AHEAD = LD * (S - 2);   // copies that may be in flight past the next step's
+    constexpr int S = C::S, BK = C::BK, NT = C::NT, CPR = C::CPR, STEPS = CPR / 2;
+    constexpr int PPC = 16 / W, LD = C::LD * PPC, LDX = C::LDX * PPC;   // pieces a chunk; pieces a thread copies a step
+    constexpr int AHEAD = LD * (S - 2);                                 // copies that may be in flight past the next step's
     __shared__ __align__(16) u32x4 lds[C::LDS];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / C::WN * C::RM, wn = wave % C::WN * C::RN;
     const int tiles = tiles_m * tiles_n;
-    const int lr = tid / CPR, lc = (tid % CPR) ^ C::swizzle(lr);   // row (of the first NT / CPR) and chunk to copy
+    // Copy i of this thread: piece tid % PPC of the stage's chunk at
+    // i * NT / PPC + tid / PPC, which holds a chunk of this row of the tile.
+    const auto row_of = [&](int i) { return (i * (NT / PPC) + tid / PPC) / CPR; };
+    const auto elem_of = [&](int i) {
+        return ((tid / PPC % CPR) ^ C::swizzle(row_of(i))) * C::C + tid % PPC * (W / (int)sizeof(T));
+    };
     // Where the copies are: tile, first element of the step, rows.
     int copy_tile = blockIdx.x, copy_k = 0;
     const T *xb, *wb;
@@ -170,21 +175,27 @@ __global__ __launch_bounds__(C::NT, 2) void linear_tile(LinearArgs a, int tiles_
 #pragma unroll
         for (int i = 0; i < LD; ++i) {
             // Rows past the end repeat the last one; their results are not stored.
-            const int r = lr + (i < C::LDX ? i : i - C::LDX) * (NT / CPR);
-            const int64_t el = i < C::LDX ? min(r, a.m - 1 - m0) * a.xs : (int64_t)min(r, a.n - 1 - n0) * a.k;
-            off[i] = (uint32_t)((el + lc * C::C) * (int)sizeof(T));
+            const int r = row_of(i);
+            const int64_t el = i < LDX ? min(r, a.m - 1 - m0) * a.xs : (int64_t)min(r - C::BM, a.n - 1 - n0) * a.k;
+            off[i] = (uint32_t)((el + elem_of(i)) * (int)sizeof(T));
         }
     };
-    // The next step's copies.  In the last step of a row a thread whose chunk
-    // lies past k copies the step's first chunk instead, and writes zeros over
+    // The next step's copies.  In the last step of a row a thread whose piece
+    // lies past k copies the step's first piece instead, and writes zeros over
     // it once it has landed.
     const auto copy = [&](int stage) {
         if (copy_tile >= tiles) return;
         u32x4* dst = lds + stage * C::STAGE;
-        const uint32_t back = copy_k + lc * C::C < a.k ? 0 : lc * 16;
+        const T *xk = uniform(xb + copy_k), *wk = uniform(wb + copy_k);
 #pragma unroll
-        for (int i = 0; i < LD; ++i)
-            copy16_to_lds((i < C::LDX ? xb : wb) + copy_k, off[i] - back, dst + i * NT + wave * 64);
+        for (int i = 0; i < LD; ++i) {
+            const T* base = i < LDX ? xk : wk;
+            const uint32_t at = off[i] - (copy_k + elem_of(i) < a.k ? 0 : elem_of(i) * (int)sizeof(T));
+            if constexpr (W == 16)
+                copy16_to_lds(base, at, dst + i * NT + wave * 64);
+            else
+                copy4_to_lds(base, at, dst + i * (NT / PPC) + wave * 16);
+        }
         copy_k += BK;
         if (copy_k >= a.k) {
             copy_k = 0;
@@ -199,9 +210,16 @@ __global__ __launch_bounds__(C::NT, 2) void linear_tile(LinearArgs a, int tiles_
             wait_vmem<AHEAD>();
         else
             wait_vmem<0>();
-        if (k0 + BK > a.k && k0 + lc * C::C >= a.k)
+        if (k0 + BK > a.k) {
 #pragma unroll
-            for (int i = 0; i < LD; ++i) lds[stage * C::STAGE + i * NT + tid] = u32x4{0, 0, 0, 0};
+            for (int i = 0; i < LD; ++i) {
+                if (k0 + elem_of(i) < a.k) continue;
+                if constexpr (W == 16)
+                    lds[stage * C::STAGE + i * NT + tid] = u32x4{0, 0, 0, 0};
+                else
+                    ((uint32_t*)(lds + stage * C::STAGE + i * (NT / PPC)))[tid] = 0;
+            }
+        }
         __syncthreads();
     };
     aim();
@@ -244,8 +262,8 @@ __global__ __launch_bounds__(C::NT, 2) void linear_tile(LinearArgs a, int tiles_
     }
 }
 
-// Any alignment, stride and k: the chunks pass through registers, one step
-// ahead.
+// Any alignment of the element and any k: the chunks pass through registers,
+// one step ahead.
 template <typename T, class C, int ACT>
 __global__ __launch_bounds__(C::NT, 2) void linear_staged(LinearArgs a, int tiles_m, int tiles_n) {
     constexpr int LD = C::LD, BK = C::BK, NT = C::NT, CPR = C::CPR;
@@ -289,15 +307,16 @@ __global__ __launch_bounds__(C::NT, 2) void linear_staged(LinearArgs a, int tile
     tile_store<T, C, ACT>(a, acc, lds + 2 * C::STAGE + wave * 256, m0 + wm, n0 + wn, lane);
 }
 
-template <typename T, bool DIRECT, int BM, int BN, int WM, int WN, int CPR, int S>
+// W: bytes of a copy, 0: through registers.
+template <typename T, int W, int BM, int BN, int WM, int WN, int CPR, int S>
 hipError_t run(const LinearArgs& a, hipStream_t s) {
     typedef Tile<T, BM, BN, WM, WN, CPR, S> C;
     const int64_t tm = ((int64_t)a.m + BM - 1) / BM, tn = ((int64_t)a.n + BN - 1) / BN;
     if (tm * tn > 0x7fff0000) return hipErrorInvalidValue;
     return with_act(a, [&](auto act) {
-        if constexpr (DIRECT) {
+        if constexpr (W > 0) {
             const int64_t fit = (int64_t)device_cu_count() * (160 * 1024 / (C::LDS * 16)) & ~7;   // workgroups at once
-            linear_tile<T, C, act()>
+            linear_tile<T, C, act(), W>
                 <<<dim3((uint32_t)(tm * tn < fit ? tm * tn : fit)), dim3(C::NT), 0, s>>>(a, (int)tm, (int)tn);
         } else {
             linear_staged<T, C, act()><<<dim3((uint32_t)(tm * tn)), dim3(C::NT), 0, s>>>(a, (int)tm, (int)tn);
@@ -306,16 +325,23 @@ hipError_t run(const LinearArgs& a, hipStream_t s) {
     });
 }
 
+template <typename T, int W>
+hipError_t run(const LinearArgs& a, linear_tile_t tile, hipStream_t s) {
+    if constexpr (sizeof(T) == 2 && W == 16)
+        if (tile == LINEAR_TILE_256) return run<T, W, 256, 256, 2, 4, 8, 2>(a, s);
+    if (tile == LINEAR_TILE_64) return run<T, W, 64, 64, 2, 2, 8, 4>(a, s);
+    // Pieces of 4 bytes always take the deep pipeline: four waves would have 32
+    // copies a step each to address (1571x770x2309 fp32: 502 us against 67).
+    if constexpr (W == 16)
+        if (tile == LINEAR_TILE_128) return run<T, W, 128, 128, 2, 2, 8, 2>(a, s);
+    return run<T, W, 128, 128, 2, 4, 8, 4>(a, s);
+}
+
 template <typename T>
 hipError_t run(const LinearArgs& a, linear_tile_t tile, hipStream_t s) {
-    if (!a.vec)
-        return tile == LINEAR_TILE_64 ? run<T, false, 64, 64, 2, 2, 8, 2>(a, s)
-                                      : run<T, false, 128, 128, 2, 2, 8, 2>(a, s);
-    if constexpr (sizeof(T) == 2)
-        if (tile == LINEAR_TILE_256) return run<T, true, 256, 256, 2, 4, 8, 2>(a, s);
-    if (tile == LINEAR_TILE_128) return run<T, true, 128, 128, 2, 2, 8, 2>(a, s);
-    if (tile == LINEAR_TILE_128_DEEP) return run<T, true, 128, 128, 2, 4, 8, 4>(a, s);
-    return run<T, true, 64, 64, 2, 2, 8, 4>(a, s);
+    if (a.vec == 16) return run<T, 16>(a, tile, s);
+    if (a.vec == 4) return run<T, 4>(a, tile, s);
+    return tile == LINEAR_TILE_64 ? run<T, 0, 64, 64, 2, 2, 8, 2>(a, s) : run<T, 0, 128, 128, 2, 2, 8, 2>(a, s);
 }
 
 }  // namespace

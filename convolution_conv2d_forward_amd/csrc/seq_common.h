@@ -60,6 +60,15 @@ __device__ __forceinline__ void store8(T* p, f32x8 v) {
     *(V*)p = __builtin_convertvector(v, V);
 }
 
+// A pointer that is the same in all lanes, in scalar registers.
+template <typename P>
+__device__ __forceinline__ P* uniform(P* p) {
+    const uint64_t v = (uint64_t)(uintptr_t)p;
+    const uint64_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+    const uint64_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32));
+    return (P*)(uintptr_t)(hi << 32 | lo);
+}
+
 // 16 bytes per lane from base + off (bytes) straight to LDS: lane l writes
 // lds + 16 l (lds wave-uniform).  Inline assembly, so that the compiler does
 // not order later LDS reads of the other stage behind it; the kernels' own
@@ -70,6 +79,14 @@ __device__ __forceinline__ void copy16_to_lds(const void* base, uint32_t off, co
 #if defined(__HIP_DEVICE_COMPILE__)
     const uint32_t m = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(m)
+                 : "memory", "m0");
+#endif
+}
+// The same for 4 bytes per lane: lane l writes lds + 4 l bytes.
+__device__ __forceinline__ void copy4_to_lds(const void* base, uint32_t off, const u32x4* lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const uint32_t m = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(m)
                  : "memory", "m0");
 #endif
 }
