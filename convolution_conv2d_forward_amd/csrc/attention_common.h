@@ -100,6 +100,14 @@ __device__ __forceinline__ ScoreP score_params(const AttnArgs& a) {
     return p;
 }
 
+// Whether a chunk holds elements whose exponent bits are all ones: one more in
+// the exponent carries into the sign's place.
+template <typename T>
+__device__ __forceinline__ bool has_bad(u32x4 v) {
+    constexpr uint32_t E = sizeof(T) == 2 ? 0x7f807f80u : 0x7f800000u, ONE = sizeof(T) == 2 ? 0x00800080u : 0x00800000u;
+    return ((((v[0] & E) + ONE) | ((v[1] & E) + ONE) | ((v[2] & E) + ONE) | ((v[3] & E) + ONE)) & (~E & (E + ONE))) != 0;
+}
+
 // Elements whose exponent bits are all ones (infinities, NaN) become zero;
 // says whether there were any.
 template <typename T>

@@ -144,10 +144,7 @@ __global__ __launch_bounds__((64 * RowsAttn<T, DP>::NW), (RowsAttn<T, DP>::OCC))
 #pragma unroll
             for (int j = 0; j < 8; ++j)
 #pragma unroll
-                for (int c = 0; c < VC; ++c) {
-                    u32x4 x = f.v[j][c];
-                    bad |= clean_chunk<T>(x);
-                }
+                for (int c = 0; c < VC; ++c) bad |= has_bad<T>(f.v[j][c]);
             bad = __ballot(bad) != 0;
         }
         if (bad) {

@@ -59,9 +59,9 @@ __device__ __forceinline__ void both_halves(float x, float& a, float& b) {
 template <typename T, int DP, int KW>
 struct TileAttn {
     static constexpr bool HALF = sizeof(T) == 2;
-    static constexpr int C = Vec<T>::chunk, BK = HALF || KW == 2 ? 64 : 32, TK = BK / 32 / KW;   // keys a tile; a wave's 32-key products
-    static constexpr int RG = 4 / KW;                                                            // 32-row groups
-    static constexpr int NC = DP / C, CPR = NC <= 4 ? 4 : NC <= 8 ? 8 : NC <= 16 ? 16 : NC <= 32 ? 32 : 64;   // chunks a row
+    static constexpr int C = Vec<T>::chunk, BK = HALF || KW == 2 ? 64 : 32;   // keys a tile
+    static constexpr int TK = BK / 32 / KW, RG = 4 / KW;   // a wave's 32-key products of a tile; 32-row groups
+    static constexpr int NC = DP / C, CPR = NC <= 4 ? 4 : NC <= 8 ? 8 : NC <= 16 ? 16 : NC <= 32 ? 32 : 64;   // of a row
     static constexpr int STAGE = 2 * BK * CPR, CP = BK * CPR / 256;   // chunks of K and V; copies of a thread for each
     static constexpr int KS = NC / 2, DT = DP / 32;
     // Stages (copies run S - 1 tiles ahead) and workgroups on a CU: what
@@ -246,7 +246,8 @@ __global__ __launch_bounds__(256, (TileAttn<T, DP, KW>::OCC)) void attention_til
                 const int r = tid / CPR + i * (256 / CPR);
                 u32x4& chunk = lds[stage * C::STAGE + BK * CPR + i * 256 + tid];
                 u32x4 v = chunk;
-                if (((tid % CPR) ^ C::swizzle(r)) < chunks && clean_chunk<T>(v)) {
+                if (((tid % CPR) ^ C::swizzle(r)) < chunks && has_bad<T>(v)) {
+                    clean_chunk<T>(v);
                     chunk = v;
                     lbad[tile & 1] = tile;
                 }
@@ -264,7 +265,6 @@ __global__ __launch_bounds__(256, (TileAttn<T, DP, KW>::OCC)) void attention_til
                 s[t] = mfma32_step<T>(*lds_ptr<const lds_u32x4>((k_at ^ 32 * i) + t * 512 * CPR), fq[i], s[t]);
         const float a1 = PLAIN ? scale : TURNED ? -2.0f * cap : 1.0f, a0 = TURNED ? cap : 0.0f;
         const float far = (float)(pos - kw - 4 * g);
-        const bool whole = kw >= f_lo && kw + 32 * TK <= f_hi;
         if (CAP || SLOPE) {
 #pragma unroll
             for (int t = 0; t < TK; ++t)
@@ -283,15 +283,19 @@ __global__ __launch_bounds__(256, (TileAttn<T, DP, KW>::OCC)) void attention_til
                     s[t][i] = x;
                 }
         }
-        if (!whole) {
-            const int from = lo - kw - 4 * g, to = hi - kw - 4 * g;
+        // Keys before and past what a row sees, each where some row needs it.
+        constexpr float NEVER = TURNED ? INFINITY : -INFINITY;
+        if (kw < f_lo) {
+            const int from = lo - kw - 4 * g;
 #pragma unroll
-            for (int t = 0; t < TK; ++t)
+            for (int i = 0; i < 16 * TK; ++i)
+                if (32 * (i >> 4) + 8 * (i >> 2 & 3) + (i & 3) < from) s[i >> 4][i & 15] = NEVER;
+        }
+        if (kw + 32 * TK > f_hi) {
+            const int to = hi - kw - 4 * g;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int key = 32 * t + 8 * (i >> 2) + (i & 3);
-                    s[t][i] = key >= from && key < to ? s[t][i] : TURNED ? INFINITY : -INFINITY;
-                }
+            for (int i = 0; i < 16 * TK; ++i)
+                if (32 * (i >> 4) + 8 * (i >> 2 & 3) + (i & 3) >= to) s[i >> 4][i & 15] = NEVER;
         }
         float top = s[0][0];
 #pragma unroll
