@@ -2,7 +2,9 @@
 
 Argument marshalling only, as for the convolutions: torch tensors give device
 memory and the current stream, the binding checks device, type, shape and
-strides against the descriptor, and passes raw pointers through the C ABI.
+strides against the descriptor (_marshal, csrc/marshal.cpp: compiled, since the
+checks in Python cost as much as the launch), and passes raw pointers through
+the C ABI.
 Sizes that a call may change (rows, tokens, batch and lengths) come from the
 tensors' shapes.
 
@@ -84,11 +86,12 @@ class _Desc:
     def __init__(self, kind, params):
         h = ctypes.c_void_p()
         _check(getattr(_lib, kind + "_desc_create")(ctypes.byref(params), ctypes.byref(h)))
-        import torch
+        if _tensor is None:
+            _load()
         self.kind, self.handle = kind, h
         self.params = type(params)()
         ctypes.memmove(ctypes.byref(self.params), ctypes.byref(params), ctypes.sizeof(params))
-        self.dtype = torch.float32 if params.dtype == DTYPE_F32 else torch.bfloat16
+        self.dtype = _f32 if params.dtype == DTYPE_F32 else _bf16
         # Kept on the instance: module globals may already be gone when the
         # last descriptors are collected at interpreter exit.
         self._destroy = getattr(_lib, kind + "_desc_destroy")
@@ -112,42 +115,17 @@ def _code(v, names):
     return int(names[v] if isinstance(v, str) else v)
 
 
-def _tensor(t, what, dtype, shape, strides):
-    """Device pointer of a GPU tensor of this type and shape whose strides are
-    those given (those of dimensions longer than 1)."""
-    if t.dtype is not dtype or not t.is_cuda:
-        raise TypeError(f"{what}: a GPU tensor of {dtype} expected, got {t.dtype} on {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.stride() != strides:
-        for n, have, want in zip(shape, t.stride(), strides):
-            if n > 1 and have != want:
-                raise ValueError(f"{what}: strides {t.stride()}, the descriptor has {tuple(strides)}")
-    return t.data_ptr()
+_tensor = None    # _marshal.tensor: the device pointer of a GPU tensor of a type, shape and strides (None: dense)
+_f32 = _bf16 = _i32 = None
 
 
-def _dense(t, what, dtype, shape):
-    """Device pointer of a dense GPU tensor of this type and shape; None stays None."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or not t.is_cuda:
-        raise TypeError(f"{what}: a GPU tensor of {dtype} expected, got {t.dtype} on {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: tensor must be contiguous")
-    return t.data_ptr()
+def _load():
+    """Types and the compiled checks of tensors, which need torch: at the first descriptor."""
+    global _tensor, _f32, _bf16, _i32
+    import torch
 
-
-_types = None
-
-
-def _torch_types():
-    global _types
-    if _types is None:
-        import torch
-        _types = torch.float32, torch.int32
-    return _types
+    from ._marshal import tensor
+    _tensor, _f32, _bf16, _i32 = tensor, torch.float32, torch.bfloat16, torch.int32
 
 
 # -------------------------------------------------------------- linear --
@@ -177,6 +155,8 @@ def linear_desc_create(params: linear_params_t) -> _Desc:
     p = d.params
     d.x_strides, d.y_strides = (p.x_stride or p.k, 1), (p.y_stride or p.n, 1)
     d.r_strides = (p.residual_stride or p.n, 1)
+    d.k, d.n, d.w_shape, d.w_strides, d.b_shape = p.k, p.n, (p.n, p.k), (p.k, 1), (p.n,)
+    d.has_bias, d.has_residual = bool(p.has_bias), bool(p.has_residual)
     return d
 
 
@@ -191,15 +171,14 @@ def linear_desc_kernel_name(desc: _Desc, rows: int) -> str:
 def linear_forward(desc: _Desc, x, w, bias, residual, y, stream=None) -> None:
     """y = act(x w^T + bias) + residual; x [rows, k], w [n, k], bias float32 [n],
     residual and y [rows, n] (y may be the residual itself)."""
-    p, dt = desc.params, desc.dtype
-    f32, _ = _torch_types()
-    rows, k, n = x.shape[0], p.k, p.n
+    dt, rows = desc.dtype, x.shape[0]
+    y_shape = (rows, desc.n)
     _check(_lib.linear_forward(
-        desc.handle, rows, _tensor(x, "x", dt, (rows, k), desc.x_strides), _tensor(w, "w", dt, (n, k), (k, 1)),
-        _dense(bias, "bias", f32, (n,)) if p.has_bias else None,
-        _tensor(residual, "residual", dt, (rows, n), desc.r_strides) if p.has_residual and residual is not None
-        else None,
-        _tensor(y, "y", dt, (rows, n), desc.y_strides), _stream(stream)))
+        desc.handle, rows, _tensor(x, "x", dt, (rows, desc.k), desc.x_strides),
+        _tensor(w, "w", dt, desc.w_shape, desc.w_strides),
+        _tensor(bias, "bias", _f32, desc.b_shape, None) if desc.has_bias else None,
+        _tensor(residual, "residual", dt, y_shape, desc.r_strides) if desc.has_residual else None,
+        _tensor(y, "y", dt, y_shape, desc.y_strides), _stream(stream)))
 
 
 # ------------------------------------------------------------- qk_rope --
@@ -231,6 +210,8 @@ def qk_rope_desc_create(params: qk_rope_params_t) -> _Desc:
     d.q_strides = (p.q_stride or p.heads_q * p.head_dim, p.head_dim, 1)
     d.k_strides = (p.k_stride or p.heads_kv * p.head_dim, p.head_dim, 1)
     d.v_strides = (p.v_stride or p.heads_kv * p.head_dim, p.head_dim, 1)
+    d.heads_q, d.heads_kv, d.head_dim, d.g_shape, d.has_norm = (p.heads_q, p.heads_kv, p.head_dim, (p.head_dim,),
+                                                                bool(p.has_norm))
     return d
 
 
@@ -243,17 +224,15 @@ def qk_rope_forward(desc: _Desc, qkv, q_gamma, k_gamma, positions, slots, q, k, 
     queries to q [tokens, heads_q, head_dim], keys and values to rows `slots`
     (None: the token's own number) of k and v [cache_rows, heads_kv, head_dim].
     positions and slots are int32; v None: values are not stored."""
-    p, dt = desc.params, desc.dtype
-    f32, i32 = _torch_types()
-    tokens, rows, hd = qkv.shape[0], k.shape[0], p.head_dim
-    kv_shape = (rows, p.heads_kv, hd)
+    dt, tokens, rows = desc.dtype, qkv.shape[0], k.shape[0]
+    token_shape, kv_shape = (tokens,), (rows, desc.heads_kv, desc.head_dim)
     _check(_lib.qk_rope_forward(
         desc.handle, tokens, _tensor(qkv, "qkv", dt, (tokens, desc.width), desc.qkv_strides),
-        _dense(q_gamma, "q_gamma", f32, (hd,)) if p.has_norm else None,
-        _dense(k_gamma, "k_gamma", f32, (hd,)) if p.has_norm else None,
-        _dense(positions, "positions", i32, (tokens,)), _dense(slots, "slots", i32, (tokens,)), rows,
-        _tensor(q, "q", dt, (tokens, p.heads_q, hd), desc.q_strides), _tensor(k, "k", dt, kv_shape, desc.k_strides),
-        None if v is None else _tensor(v, "v", dt, kv_shape, desc.v_strides), _stream(stream)))
+        _tensor(q_gamma, "q_gamma", _f32, desc.g_shape, None) if desc.has_norm else None,
+        _tensor(k_gamma, "k_gamma", _f32, desc.g_shape, None) if desc.has_norm else None,
+        _tensor(positions, "positions", _i32, token_shape, None), _tensor(slots, "slots", _i32, token_shape, None), rows,
+        _tensor(q, "q", dt, (tokens, desc.heads_q, desc.head_dim), desc.q_strides),
+        _tensor(k, "k", dt, kv_shape, desc.k_strides), _tensor(v, "v", dt, kv_shape, desc.v_strides), _stream(stream)))
 
 
 # ----------------------------------------------------------- attention --
@@ -282,6 +261,7 @@ def attention_desc_create(params: attention_params_t) -> _Desc:
     d = _Desc("attention", params)
     p = d.params
     d.strides = [tuple(s) + (1,) for s in (p.q_strides, p.k_strides, p.v_strides, p.out_strides)]
+    d.heads_q, d.heads_kv, d.head_dim, d.has_slopes = p.heads_q, p.heads_kv, p.head_dim, bool(p.has_slopes)
     return d
 
 
@@ -302,21 +282,21 @@ def attention_forward(desc: _Desc, q, k, v, out, *, q_lens=None, kv_lens=None, p
     int32 [batch]; doc_offsets: int32 [batch, documents + 1]; slopes: float32
     [heads_q]; workspace: a tensor of attention_workspace_bytes, or None where
     that is 0."""
-    p, dt = desc.params, desc.dtype
-    f32, i32 = _torch_types()
-    batch, q_len, kv_len = q.shape[0], q.shape[1], k.shape[1]
-    q_shape, k_shape = (batch, q_len, p.heads_q, p.head_dim), (batch, kv_len, p.heads_kv, p.head_dim)
+    dt, hd = desc.dtype, desc.head_dim
+    (batch, q_len), kv_len = q.shape[:2], k.shape[1]
+    q_shape, k_shape, b_shape = (batch, q_len, desc.heads_q, hd), (batch, kv_len, desc.heads_kv, hd), (batch,)
     sq, sk, sv, so = desc.strides
-    n_docs = 0
+    n_docs, ws, ws_bytes = 0, None, 0
     if doc_offsets is not None:
         n_docs = doc_offsets.shape[-1] - 1
-    if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
-        raise ValueError("workspace: contiguous GPU tensor expected")
+    if workspace is not None:
+        if not (workspace.is_cuda and workspace.is_contiguous()):
+            raise ValueError("workspace: contiguous GPU tensor expected")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(_lib.attention_forward(
         desc.handle, batch, q_len, kv_len, _tensor(q, "q", dt, q_shape, sq), _tensor(k, "k", dt, k_shape, sk),
-        _tensor(v, "v", dt, k_shape, sv), _dense(q_lens, "q_lens", i32, (batch,)),
-        _dense(kv_lens, "kv_lens", i32, (batch,)), _dense(prefix_lens, "prefix_lens", i32, (batch,)),
-        _dense(doc_offsets, "doc_offsets", i32, (batch, n_docs + 1)), n_docs,
-        _dense(slopes, "slopes", f32, (p.heads_q,)) if p.has_slopes else None, _tensor(out, "out", dt, q_shape, so),
-        workspace.data_ptr() if workspace is not None else None,
-        workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream)))
+        _tensor(v, "v", dt, k_shape, sv), _tensor(q_lens, "q_lens", _i32, b_shape, None),
+        _tensor(kv_lens, "kv_lens", _i32, b_shape, None), _tensor(prefix_lens, "prefix_lens", _i32, b_shape, None),
+        _tensor(doc_offsets, "doc_offsets", _i32, (batch, n_docs + 1), None), n_docs,
+        _tensor(slopes, "slopes", _f32, (desc.heads_q,), None) if desc.has_slopes else None,
+        _tensor(out, "out", dt, q_shape, so), ws, ws_bytes, _stream(stream)))

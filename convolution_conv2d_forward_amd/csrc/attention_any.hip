@@ -395,7 +395,11 @@ AttnPlan plan_attention(int32_t dtype, const AttnArgs& a) {
     p.row_tiles = (a.rows + tile - 1) / tile;
     // Few row tiles leave compute units without work: the keys are then split.
     const int64_t tiles = (int64_t)a.batch * a.heads_kv * p.row_tiles, cus = device_cu_count();
-    int64_t want = p.kernel == ATTN_TILE_64 ? cus : 2 * cus, keys = 256;   // workgroups, and keys for each at least
+    // Workgroups wanted, and keys for each at least.  The partial results of
+    // many rows cost as much as a few hundred keys of bf16: 1000 causal rows of
+    // 16 heads of 128 over 4 take 22.8 us undivided, 27.5 in two.
+    int64_t want = p.kernel == ATTN_TILE_64 ? cus : 2 * cus;
+    int64_t keys = dtype != CONV_DTYPE_F32 && tiles * 2 >= cus ? 1024 : 256;
     if (p.kernel == ATTN_ROWS) {
         // Two workgroups fit on a unit (one where a row of K has more than 256
         // bytes); a third per unit evens out sequences of different lengths.
