@@ -214,7 +214,7 @@ hipError_t run_vec(const RopeArgs& a, hipStream_t s) {
     // A wave takes all heads of its token where the tokens alone make enough
     // waves; few tokens (a step of single tokens) spread a token's heads over
     // up to `steps` waves.
-    const int64_t want = (int64_t)device_cu_count() * 8;
+    const int64_t want = (int64_t)device_cu_count() * 32;
     int64_t parts = (want + a.tokens - 1) / a.tokens;
     if (parts > steps) parts = steps;
     const int64_t waves = (int64_t)a.tokens * parts;
