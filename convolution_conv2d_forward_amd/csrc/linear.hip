@@ -1,16 +1,23 @@
 // Dispatch of linear_forward.
+#include <cmath>
+
 #include "linear_common.h"
 
 namespace conv2d {
 
 namespace {
 
-// The kernel of a call, by sizes and type alone.  Few rows go to linear_rows,
-// whose workgroups read 16 rows of w and all of x: up to 32 rows always, up to
-// 128 while x is not read too often (64x4096x4096: 14.8 us against 23.2 in
-// tiles; 64x4096x11264: 35.3 against 28.0).  Else the tile whose workgroups
-// are expected to end first: rounds of workgroups times the time of a step,
-// measured (us) with all CUs at work:
+// The kernel of a call, by sizes, type and alignment: the one that is expected
+// to end first.
+//
+// linear_rows reads 16 rows of w and up to 64 of x per workgroup (32 where
+// rows start at no 4-byte boundary), and deals k among its waves: us for each
+// 128-byte unit of a wave, alone and with all CUs at work, after some 5 us.
+// It takes up to 32 rows always, and few tiles of a long k (64x4096x4096: 14.8
+// us against 23.2 in tiles; 64x4096x11264: 35.3 against 28.0).
+//
+// Tiles take rounds of workgroups, and in each for a step of 128 bytes (us,
+// with all CUs at work), after some 6 us:
 //              256    128 by pairs    128 deep    64
 //   bf16       1.9    1.2             0.72        0.49, one a CU 0.30
 //   fp32       -      3.85            2.07        1.1, one a CU 0.65
@@ -18,13 +25,12 @@ namespace {
 // deep ones, 129 in tiles of 64.)
 linear_tile_t pick(int32_t dtype, const LinearArgs& a) {
     if (a.m <= 32) return LINEAR_ROWS;
-    if (a.m <= 128 && a.vec == 16 && (int64_t)((a.n + 15) / 16) * ((a.m + 15) / 16 + 1) <= 2304) return LINEAR_ROWS;
+    const bool f32 = dtype == CONV_DTYPE_F32;
     const int64_t cus = device_cu_count();
     const auto rounds = [&](int64_t t, int64_t per_cu) {
         const int64_t tiles = ((a.m + t - 1) / t) * ((a.n + t - 1) / t);
         return (float)((tiles + cus * per_cu - 1) / (cus * per_cu));
     };
-    const bool f32 = dtype == CONV_DTYPE_F32;
     float best = rounds(64, 1) == 1 ? (f32 ? 0.65f : 0.30f) : rounds(64, 2) * (f32 ? 1.1f : 0.49f);
     linear_tile_t tile = LINEAR_TILE_64;
     const auto offer = [&](linear_tile_t t, float cost) {
@@ -36,6 +42,12 @@ linear_tile_t pick(int32_t dtype, const LinearArgs& a) {
     offer(LINEAR_TILE_128_DEEP, rounds(128, 1) * (f32 ? 2.07f : 0.72f));
     offer(LINEAR_TILE_128, rounds(128, 2) * (f32 ? 3.85f : 1.2f));
     if (!f32) offer(LINEAR_TILE_256, rounds(256, 1) * 1.9f);
+    const int bytes = a.k * (f32 ? 4 : 2), rows = a.vec ? 64 : 32, waves = a.vec ? 4 : 8;
+    const float groups = (float)((a.m + rows - 1) / rows) * (float)((a.n + 15) / 16) / (float)cus;
+    const float unit = a.vec ? fmaxf(0.33f, 0.6f * groups) : fmaxf(1.2f, 1.8f * groups);
+    const float step = a.vec ? best : best * 1.5f;   // through registers
+    if (5.0f + (float)((bytes + 128 * waves - 1) / (128 * waves)) * unit < 6.0f + (float)((bytes + 127) / 128) * step)
+        return LINEAR_ROWS;
     return tile;
 }
 

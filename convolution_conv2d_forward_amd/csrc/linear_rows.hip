@@ -17,10 +17,10 @@ __device__ __forceinline__ void linear_act_any(const LinearArgs& a, float* v) {
     }
 }
 
-// The waves' sums meet in LDS, and 16 NT x 16 MT outputs from column n0 on are
-// formed and stored.
+// The waves' sums meet in LDS, and 16 NT x 16 MT outputs from row m0 and
+// column n0 on are formed and stored.
 template <typename T, int MT, int NT, int NW>
-__device__ __forceinline__ void rows_store(const LinearArgs& a, const f32x4 (&acc)[NT][MT], f32x4* red, int n0,
+__device__ __forceinline__ void rows_store(const LinearArgs& a, const f32x4 (&acc)[NT][MT], f32x4* red, int m0, int n0,
                                            int wave, int lane) {
     const int r = lane & 15, g = lane >> 4;
 #pragma unroll
@@ -29,7 +29,7 @@ __device__ __forceinline__ void rows_store(const LinearArgs& a, const f32x4 (&ac
         for (int j = 0; j < MT; ++j) red[(wave * NT * MT + i * MT + j) * 64 + lane] = acc[i][j];
     __syncthreads();
     for (int t = wave; t < NT * MT; t += NW) {
-        const int m = 16 * (t % MT) + r, n = n0 + 16 * (t / MT) + 4 * g;
+        const int m = m0 + 16 * (t % MT) + r, n = n0 + 16 * (t / MT) + 4 * g;
         if (m >= a.m || n >= a.n) continue;
         T* y = (T*)a.y + m * a.ys + n;
         const T* res = a.residual ? (const T*)a.residual + m * a.rs + n : nullptr;
@@ -53,22 +53,22 @@ __device__ __forceinline__ void rows_store(const LinearArgs& a, const f32x4 (&ac
     }
 }
 
-// 16 NT rows of w against all of x (up to 16 MT rows) per workgroup.  Its NW
+// 16 NT rows of w against 16 MT rows of x per workgroup.  Its NW
 // waves deal the 128-byte units of the rows among themselves; every lane reads
 // its chunks of w and x straight into the operands of the matrix cores, U
 // units in flight at a time.
 template <typename T, int MT, int NT, int NW, int U>
-__global__ __launch_bounds__(64 * NW) void linear_rows(LinearArgs a) {
+__global__ __launch_bounds__(64 * NW) void linear_rows(LinearArgs a, int blocks_m) {
     constexpr int C = Vec<T>::chunk, UNIT = 8 * C;
     __shared__ __align__(16) f32x4 red[NW * NT * MT * 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int n0 = blockIdx.x * 16 * NT, r = lane & 15, g = lane >> 4;
+    const int m0 = blockIdx.x % blocks_m * 16 * MT, n0 = blockIdx.x / blocks_m * 16 * NT, r = lane & 15, g = lane >> 4;
     // Rows past the end repeat the last one; their results are not stored.
     const T *w[NT], *x[MT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) w[i] = (const T*)a.w + (int64_t)min(n0 + 16 * i + r, a.n - 1) * a.k + g * C;
 #pragma unroll
-    for (int j = 0; j < MT; ++j) x[j] = (const T*)a.x + (int64_t)min(16 * j + r, a.m - 1) * a.xs + g * C;
+    for (int j = 0; j < MT; ++j) x[j] = (const T*)a.x + (int64_t)min(m0 + 16 * j + r, a.m - 1) * a.xs + g * C;
     f32x4 acc[NT][MT] = {};
     for (int k0 = wave * UNIT; k0 < a.k; k0 += NW * U * UNIT) {
         u32x4 fw[U][2][NT], fx[U][2][MT];
@@ -78,9 +78,9 @@ __global__ __launch_bounds__(64 * NW) void linear_rows(LinearArgs a) {
             for (int h = 0; h < 2; ++h) {
                 const int k = k0 + u * NW * UNIT + h * 4 * C, left = a.k - k - g * C;   // elements from this lane's first
 #pragma unroll
-                for (int i = 0; i < NT; ++i) fw[u][h][i] = load_chunk<T>(w[i] + k, left);
+                for (int i = 0; i < NT; ++i) fw[u][h][i] = load_words(w[i] + k, left);
 #pragma unroll
-                for (int j = 0; j < MT; ++j) fx[u][h][j] = load_chunk<T>(x[j] + k, left);
+                for (int j = 0; j < MT; ++j) fx[u][h][j] = load_words(x[j] + k, left);
             }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -91,43 +91,50 @@ __global__ __launch_bounds__(64 * NW) void linear_rows(LinearArgs a) {
 #pragma unroll
                     for (int j = 0; j < MT; ++j) acc[i][j] = mfma_step<T>(fw[u][h][i], fx[u][h][j], acc[i][j]);
     }
-    rows_store<T, MT, NT, NW>(a, acc, red, n0, wave, lane);
+    rows_store<T, MT, NT, NW>(a, acc, red, m0, n0, wave, lane);
 }
 
 // The same through LDS: every wave has a ring of S stages of its own, each one
-// unit of all rows, and copies S - 1 units ahead of its products; the copies
-// move whole 128-byte lines, where the operands' layout makes register loads
-// take 64 bytes of 16 rows at a time.
-template <typename T, int MT, int NT, int NW, int S>
-__global__ __launch_bounds__(64 * NW) void linear_rows_ring(LinearArgs a) {
-    constexpr int C = Vec<T>::chunk, UNIT = 8 * C, ROWS = 16 * (NT + MT), LD = ROWS / 8;
+// unit of all rows, and copies S - 1 units ahead of its products, in pieces of
+// W bytes; the copies move whole 128-byte lines, where the operands' layout
+// makes register loads take 64 bytes of 16 rows at a time.
+template <typename T, int MT, int NT, int NW, int S, int W>
+__global__ __launch_bounds__(64 * NW) void linear_rows_ring(LinearArgs a, int blocks_m) {
+    constexpr int C = Vec<T>::chunk, UNIT = 8 * C, ROWS = 16 * (NT + MT), PPC = 16 / W, LD = ROWS / 8 * PPC;
     constexpr int RING = NW * S * ROWS * 8, RED = NW * NT * MT * 64;
     __shared__ __align__(16) u32x4 lds[RING > RED ? RING : RED];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n0 = blockIdx.x * 16 * NT, r = lane & 15, g = lane >> 4;
+    const int m0 = blockIdx.x % blocks_m * 16 * MT, n0 = blockIdx.x / blocks_m * 16 * NT, r = lane & 15, g = lane >> 4;
     u32x4* ring = lds + wave * S * ROWS * 8;
-    // Copy i takes rows 8 i .. 8 i + 7 of the stage: first w's, then x's.
-    // Chunk c of row i is stored at c ^ (i / 2 % 8).
-    const int lr = lane >> 3;
+    // Copy i of this lane: piece lane % PPC of the stage's chunk at
+    // i * 64 / PPC + lane / PPC; rows of w come first, then x's.  Chunk c of
+    // row i is stored at c ^ (i / 2 % 8).
+    const auto row_of = [&](int i) { return (i * (64 / PPC) + lane / PPC) / 8; };
+    const auto elem_of = [&](int i) {
+        return ((lane / PPC % 8) ^ ((row_of(i) >> 1) & 7)) * C + lane % PPC * (W / (int)sizeof(T));
+    };
     uint32_t off[LD];
-    int lc[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) lc[i] = (lane & 7) ^ (((8 * i + lr) >> 1) & 7);
 #pragma unroll
     for (int i = 0; i < LD; ++i) {
-        const int row = 8 * i + lr;
-        const int64_t el = i < 2 * NT ? (int64_t)(min(n0 + row, a.n - 1) - n0) * a.k
-                                      : min(row - 16 * NT, a.m - 1) * a.xs;
-        off[i] = (uint32_t)((el + lc[i & 1] * C) * (int)sizeof(T));
+        const int row = row_of(i);
+        const int64_t el = i < 2 * NT * PPC ? (int64_t)(min(n0 + row, a.n - 1) - n0) * a.k
+                                            : min(row - 16 * NT, a.m - 1 - m0) * a.xs;
+        off[i] = (uint32_t)((el + elem_of(i)) * (int)sizeof(T));
     }
-    const T *wb = (const T*)a.w + (int64_t)n0 * a.k, *xb = (const T*)a.x;
-    // A chunk past k is copied from the unit's start, and zeros are written over it.
+    const T *wb = (const T*)a.w + (int64_t)n0 * a.k, *xb = (const T*)a.x + (int64_t)m0 * a.xs;
+    // A piece past k is copied from the unit's start, and zeros are written over it.
     const auto copy = [&](int k0, int stage) {
         if (k0 >= a.k) return;
+        const T *wk = uniform(wb + k0), *xk = uniform(xb + k0);
+        const u32x4* dst = ring + stage * ROWS * 8;
 #pragma unroll
         for (int i = 0; i < LD; ++i) {
-            const uint32_t back = k0 + lc[i & 1] * C < a.k ? 0 : lc[i & 1] * 16;
-            copy16_to_lds((i < 2 * NT ? wb : xb) + k0, off[i] - back, ring + stage * ROWS * 8 + i * 64);
+            const T* base = i < 2 * NT * PPC ? wk : xk;
+            const uint32_t at = off[i] - (k0 + elem_of(i) < a.k ? 0 : elem_of(i) * (int)sizeof(T));
+            if constexpr (W == 16)
+                copy16_to_lds(base, at, dst + i * 64);
+            else
+                copy4_to_lds(base, at, dst + i * 16);
         }
     };
     f32x4 acc[NT][MT] = {};
@@ -143,8 +150,13 @@ __global__ __launch_bounds__(64 * NW) void linear_rows_ring(LinearArgs a) {
         u32x4* st = ring + stage * ROWS * 8;
         if (k0 + UNIT > a.k) {
 #pragma unroll
-            for (int i = 0; i < LD; ++i)
-                if (k0 + lc[i & 1] * C >= a.k) st[i * 64 + lane] = u32x4{0, 0, 0, 0};
+            for (int i = 0; i < LD; ++i) {
+                if (k0 + elem_of(i) < a.k) continue;
+                if constexpr (W == 16)
+                    st[i * 64 + lane] = u32x4{0, 0, 0, 0};
+                else
+                    ((uint32_t*)(st + i * 16))[lane] = 0;
+            }
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -169,34 +181,45 @@ __global__ __launch_bounds__(64 * NW) void linear_rows_ring(LinearArgs a) {
         stage = stage == S - 1 ? 0 : stage + 1;
     }
     __syncthreads();
-    rows_store<T, MT, NT, NW>(a, acc, (f32x4*)lds, n0, wave, lane);
+    rows_store<T, MT, NT, NW>(a, acc, (f32x4*)lds, m0, n0, wave, lane);
 }
 
-template <typename T, int MT, int NT, int NW, int U>
-hipError_t run(const LinearArgs& a, hipStream_t s) {
-    const dim3 grid((uint32_t)((a.n + 16 * NT - 1) / (16 * NT))), block(64 * NW);
-    linear_rows<T, MT, NT, NW, U><<<grid, block, 0, s>>>(a);
-    return hipGetLastError();
+template <int MT, int NT>
+dim3 grid_of(const LinearArgs& a, int& blocks_m) {
+    blocks_m = (a.m + 16 * MT - 1) / (16 * MT);
+    return dim3((uint32_t)((int64_t)blocks_m * ((a.n + 16 * NT - 1) / (16 * NT))));
 }
 
-template <typename T, int MT, int NT, int NW, int S>
+template <typename T, int MT, int NT, int NW, int S, int W>
 hipError_t run_ring(const LinearArgs& a, hipStream_t s) {
-    linear_rows_ring<T, MT, NT, NW, S><<<dim3((uint32_t)((a.n + 16 * NT - 1) / (16 * NT))), dim3(64 * NW), 0, s>>>(a);
+    int blocks_m;
+    const dim3 grid = grid_of<MT, NT>(a, blocks_m);
+    linear_rows_ring<T, MT, NT, NW, S, W><<<grid, dim3(64 * NW), 0, s>>>(a, blocks_m);
     return hipGetLastError();
+}
+
+template <typename T, int W>
+hipError_t run_ring(const LinearArgs& a, hipStream_t s) {
+    // Waves, stages: the fastest of those tried at 1 to 128 rows, among them
+    // 16 waves, 2 to 8 stages and 32 or 64 rows of w a workgroup.
+    if (a.m <= 16) return run_ring<T, 1, 1, 8, 2, W>(a, s);
+    if (a.m <= 32) return run_ring<T, 2, 1, 4, W == 16 ? 3 : 2, W>(a, s);
+    return run_ring<T, 4, 1, 4, 2, W>(a, s);
 }
 
 template <typename T>
 hipError_t run(const LinearArgs& a, hipStream_t s) {
-    if (a.vec == 16) {
-        // Waves, stages: the fastest of those tried at 1 to 128 rows, among
-        // them 16 waves, 2 to 8 stages and 32 or 64 rows of w a workgroup.
-        if (a.m <= 16) return run_ring<T, 1, 1, 8, 2>(a, s);
-        if (a.m <= 32) return run_ring<T, 2, 1, 4, 3>(a, s);
-        if (a.m <= 64) return run_ring<T, 4, 1, 4, 2>(a, s);
-        return run_ring<T, 8, 1, 4, 2>(a, s);
+    if (a.vec == 16) return run_ring<T, 16>(a, s);
+    if (a.vec == 4) return run_ring<T, 4>(a, s);
+    int blocks_m;
+    if (a.m <= 16) {
+        const dim3 grid = grid_of<1, 1>(a, blocks_m);
+        linear_rows<T, 1, 1, 8, 4><<<grid, dim3(512), 0, s>>>(a, blocks_m);
+    } else {
+        const dim3 grid = grid_of<2, 1>(a, blocks_m);
+        linear_rows<T, 2, 1, 8, 2><<<grid, dim3(512), 0, s>>>(a, blocks_m);
     }
-    if (a.m <= 16) return run<T, 1, 1, 8, 4>(a, s);
-    return run<T, 2, 1, 8, 2>(a, s);
+    return hipGetLastError();
 }
 
 }  // namespace

@@ -49,6 +49,18 @@ struct Frags {
     }
 };
 
+// Up to 8 elements from p on, of which `left` are there (at any alignment).
+template <typename V, typename E>
+__device__ __forceinline__ void load_some(V* v, const E* p, int left) {
+    if (left >= 8) {
+        __builtin_memcpy(v, p, 8 * sizeof(E));
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < left) (*v)[e] = p[e];
+}
+
 // Outputs pass through 4 KB of LDS of the wave's own, 32x32 at a time, so that
 // global memory is read and written along rows; the residuals of a column of
 // blocks are in flight before the first is used.
@@ -68,72 +80,52 @@ __device__ __forceinline__ void tile_store(const LinearArgs& a, const f32x16 (&a
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     };
-    if (a.vec_out) {
-        // A lane takes 8 columns of rows lane / 4 and lane / 4 + 16.
-        typedef T V __attribute__((ext_vector_type(8)));
-        const int r0 = lane >> 2, c0 = lane & 3;
-#pragma unroll
-        for (int i = 0; i < C::NI; ++i) {
-            const int nn = n + 32 * i + 8 * c0;
-            V res[C::MI][2] = {};
-            if (a.residual)
-#pragma unroll
-                for (int j = 0; j < C::MI; ++j)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int mm = m + 32 * j + r0 + 16 * h;
-                        if (mm < a.m && nn < a.n) res[j][h] = *(const V*)((const T*)a.residual + mm * a.rs + nn);
-                    }
-            f32x8 b{};
-            if (a.bias && nn < a.n) __builtin_memcpy(&b, a.bias + nn, 32);
-#pragma unroll
-            for (int j = 0; j < C::MI; ++j) {
-                put(acc[i][j]);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float v[8];
-                    __builtin_memcpy(v, &os[at(r0 + 16 * h, 2 * c0)], 16);
-                    __builtin_memcpy(v + 4, &os[at(r0 + 16 * h, 2 * c0 + 1)], 16);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] += b[e];
-                    linear_act<ACT, 8>(a, v);
-                    const f32x8 r = __builtin_convertvector(res[j][h], f32x8);
-                    f32x8 o;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = v[e] + r[e];
-                    const int mm = m + 32 * j + r0 + 16 * h;
-                    V w = __builtin_convertvector(o, V);
-                    // Formed by all lanes: a residual left unused in a branch
-                    // not taken would make the product loop wait for memory.
-                    asm volatile("" : "+v"(w));
-                    if (mm < a.m && nn < a.n) *(V*)((T*)a.y + mm * a.ys + nn) = w;
-                }
-            }
-        }
-        return;
-    }
-    // A lane takes one column of 16 rows.
+    // A lane takes 8 columns of rows lane / 4 and lane / 4 + 16, at any
+    // alignment; chunks that the row's end cuts go element by element.
+    typedef T V __attribute__((ext_vector_type(8)));
+    const int r0 = lane >> 2, c0 = lane & 3;
 #pragma unroll
     for (int i = 0; i < C::NI; ++i) {
-        const int c = lane & 31, nn = n + 32 * i + c;
-        const float b = a.bias && nn < a.n ? a.bias[nn] : 0.0f;
+        const int nn = n + 32 * i + 8 * c0, left = a.n - nn;
+        V res[C::MI][2] = {};
+        if (a.residual)
+#pragma unroll
+            for (int j = 0; j < C::MI; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int mm = m + 32 * j + r0 + 16 * h;
+                    if (mm < a.m) load_some(&res[j][h], (const T*)a.residual + mm * a.rs + nn, left);
+                }
+        f32x8 b{};
+        if (a.bias) load_some(&b, a.bias + nn, left);
 #pragma unroll
         for (int j = 0; j < C::MI; ++j) {
-            const int m1 = m + 32 * j + (lane >> 5) * 16;
-            float v[16], res[16] = {};
-            if (a.residual)
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (m1 + e < a.m && nn < a.n) res[e] = to_f32(((const T*)a.residual)[(m1 + e) * a.rs + nn]);
             put(acc[i][j]);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = ((const float*)&os[at((lane >> 5) * 16 + e, c >> 2)])[c & 3] + b;
-            linear_act<ACT, 16>(a, v);
+            for (int h = 0; h < 2; ++h) {
+                float v[8];
+                __builtin_memcpy(v, &os[at(r0 + 16 * h, 2 * c0)], 16);
+                __builtin_memcpy(v + 4, &os[at(r0 + 16 * h, 2 * c0 + 1)], 16);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                float w = v[e] + res[e];
-                asm volatile("" : "+v"(w));   // as above
-                if (m1 + e < a.m && nn < a.n) ((T*)a.y)[(m1 + e) * a.ys + nn] = from_f32<T>(w);
+                for (int e = 0; e < 8; ++e) v[e] += b[e];
+                linear_act<ACT, 8>(a, v);
+                const f32x8 r = __builtin_convertvector(res[j][h], f32x8);
+                f32x8 o;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = v[e] + r[e];
+                const int mm = m + 32 * j + r0 + 16 * h;
+                V w = __builtin_convertvector(o, V);
+                // Formed by all lanes: a residual left unused in a branch
+                // not taken would make the product loop wait for memory.
+                asm volatile("" : "+v"(w));
+                T* y = (T*)a.y + mm * a.ys + nn;
+                if (mm < a.m && left >= 8) {
+                    __builtin_memcpy(y, &w, sizeof(w));
+                } else if (mm < a.m) {
+#pragma unroll
+                    for (int e = 0; e < 7; ++e)
+                        if (e < left) y[e] = w[e];
+                }
             }
         }
     }

@@ -24,14 +24,17 @@ def cc():
     (17, 136, 100, "bf16", "linear_rows_bf16"), (40, 2056, 200, "bf16", "linear_rows_bf16"),
     (64, 72, 1000, "f32", "linear_rows_f32"), (65, 264, 130, "bf16", "linear_rows_bf16"),
     (128, 520, 48, "bf16", "linear_rows_bf16"), (100, 100, 33, "f32", "linear_rows_f32"),
-    (200, 328, 264, "bf16", "linear_tile_bf16/64"), (129, 36, 100, "f32", "linear_tile_f32/64"),
+    (200, 328, 264, "bf16", "linear_rows_bf16"), (129, 36, 100, "f32", "linear_rows_f32"),
+    (1000, 72, 1000, "bf16", "linear_tile_bf16/64"), (1000, 32, 1000, "f32", "linear_tile_f32/64"),
     (1000, 136, 4000, "bf16", "linear_tile_bf16/128deep"), (2000, 44, 2000, "f32", "linear_tile_f32/128deep"),
     (2000, 72, 4000, "bf16", "linear_tile_bf16/128"), (4090, 72, 4088, "bf16", "linear_tile_bf16/256"),
     (4096, 8, 4090, "bf16", "linear_tile_bf16/256"),
     # Rows at 4-byte boundaries, and at none.
     (300, 66, 257, "bf16", "linear_tile_bf16/64"), (2000, 70, 3001, "bf16", "linear_tile_bf16/128"),
     (300, 37, 65, "f32", "linear_tile_f32/64"), (1990, 33, 2001, "f32", "linear_tile_f32/128deep"),
-    (300, 67, 130, "bf16", "linear_tile_bf16/64"), (2000, 35, 3001, "bf16", "linear_tile_bf16/128"),
+    (300, 67, 130, "bf16", "linear_tile_bf16/64"), (70, 515, 100, "bf16", "linear_rows_bf16"),
+    (70, 514, 100, "bf16", "linear_rows_bf16"), (33, 515, 49, "f32", "linear_rows_f32"),
+    (2000, 35, 3001, "bf16", "linear_tile_bf16/128"),
     (50, 33, 40, "bf16", "linear_tile_bf16/64"),
 ])
 @pytest.mark.parametrize("act", ["none", "gelu"])
