@@ -10,11 +10,14 @@ namespace {
 // The kernel of a call, by sizes, type and alignment: the one that is expected
 // to end first.
 //
-// linear_rows reads 16 rows of w and up to 64 of x per workgroup (32 where
-// rows start at no 4-byte boundary), and deals k among its waves: us for each
-// 128-byte unit of a wave, alone and with all CUs at work, after some 5 us.
-// It takes up to 32 rows always, and few tiles of a long k (64x4096x4096: 14.8
-// us against 23.2 in tiles; 64x4096x11264: 35.3 against 28.0).
+// linear_rows deals k among a workgroup's waves (its shape: rows_shape).  After
+// some 5 us each 128-byte unit of a wave takes (us)
+//   one workgroup a CU, 16 / 32 / 64 rows    bf16 0.3 / 0.25 / 0.33
+//                                            fp32 0.3 / 0.55 / 0.6
+//   for each workgroup a CU has, 64 rows     0.6 and 1.4
+// and through registers 1.2, or 1.8 for each with 32 rows.  It takes up to 32
+// rows always, and few tiles of a long k (64x4096x4096 bf16: 14.8 us against
+// 23.2 in tiles; 64x4096x11264: 35.3 against 28.0).
 //
 // Tiles take rounds of workgroups, and in each for a step of 128 bytes (us,
 // with all CUs at work), after some 6 us:
@@ -42,9 +45,11 @@ linear_tile_t pick(int32_t dtype, const LinearArgs& a) {
     offer(LINEAR_TILE_128_DEEP, rounds(128, 1) * (f32 ? 2.07f : 0.72f));
     offer(LINEAR_TILE_128, rounds(128, 2) * (f32 ? 3.85f : 1.2f));
     if (!f32) offer(LINEAR_TILE_256, rounds(256, 1) * 1.9f);
-    const int bytes = a.k * (f32 ? 4 : 2), rows = a.vec ? 64 : 32, waves = a.vec ? 4 : 8;
+    const RowsShape sh = rows_shape(f32, a);
+    const int bytes = a.k * (f32 ? 4 : 2), rows = 16 * sh.mt, waves = sh.waves;
     const float groups = (float)((a.m + rows - 1) / rows) * (float)((a.n + 15) / 16) / (float)cus;
-    const float unit = a.vec ? fmaxf(0.33f, 0.6f * groups) : fmaxf(1.2f, 1.8f * groups);
+    const float alone = !a.vec ? 1.2f : sh.mt == 4 ? (f32 ? 0.6f : 0.33f) : sh.mt == 2 ? (f32 ? 0.55f : 0.25f) : 0.3f;
+    const float unit = fmaxf(alone, groups * (float)sh.mt * (!a.vec ? 0.9f : f32 ? 0.35f : 0.15f));
     const float step = a.vec ? best : best * 1.5f;   // through registers
     if (5.0f + (float)((bytes + 128 * waves - 1) / (128 * waves)) * unit < 6.0f + (float)((bytes + 127) / 128) * step)
         return LINEAR_ROWS;

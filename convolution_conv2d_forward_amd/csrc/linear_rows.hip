@@ -200,11 +200,14 @@ hipError_t run_ring(const LinearArgs& a, hipStream_t s) {
 
 template <typename T, int W>
 hipError_t run_ring(const LinearArgs& a, hipStream_t s) {
-    // Waves, stages: the fastest of those tried at 1 to 128 rows, among them
-    // 16 waves, 2 to 8 stages and 32 or 64 rows of w a workgroup.
-    if (a.m <= 16) return run_ring<T, 1, 1, 8, 2, W>(a, s);
-    if (a.m <= 32) return run_ring<T, 2, 1, 4, W == 16 ? 3 : 2, W>(a, s);
-    return run_ring<T, 4, 1, 4, 2, W>(a, s);
+    // Stages: the fastest of 2 to 8; 16 waves and 32 or 64 rows of w a
+    // workgroup were slower or equal at 1 to 128 rows.
+    const RowsShape sh = rows_shape(sizeof(T) == 4, a);
+    if (sh.mt == 1) return run_ring<T, 1, 1, 8, 2, W>(a, s);
+    if (sh.mt == 4) return run_ring<T, 4, 1, 4, 2, W>(a, s);
+    if constexpr (sizeof(T) == 4)
+        if (sh.waves == 8) return run_ring<T, 2, 1, 8, 2, W>(a, s);
+    return run_ring<T, 2, 1, 4, W == 16 ? 3 : 2, W>(a, s);
 }
 
 template <typename T>
@@ -212,7 +215,7 @@ hipError_t run(const LinearArgs& a, hipStream_t s) {
     if (a.vec == 16) return run_ring<T, 16>(a, s);
     if (a.vec == 4) return run_ring<T, 4>(a, s);
     int blocks_m;
-    if (a.m <= 16) {
+    if (rows_shape(sizeof(T) == 4, a).mt == 1) {
         const dim3 grid = grid_of<1, 1>(a, blocks_m);
         linear_rows<T, 1, 1, 8, 4><<<grid, dim3(512), 0, s>>>(a, blocks_m);
     } else {

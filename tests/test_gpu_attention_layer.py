@@ -25,6 +25,10 @@ def cc():
     (64, 72, 1000, "f32", "linear_rows_f32"), (65, 264, 130, "bf16", "linear_rows_bf16"),
     (128, 520, 48, "bf16", "linear_rows_bf16"), (100, 100, 33, "f32", "linear_rows_f32"),
     (200, 328, 264, "bf16", "linear_rows_bf16"), (129, 36, 100, "f32", "linear_rows_f32"),
+    (46, 264, 100, "f32", "linear_rows_f32"), (100, 136, 600, "f32", "linear_rows_f32"),
+    (100, 134, 600, "bf16", "linear_rows_bf16"), (100, 133, 600, "f32", "linear_rows_f32"),
+    (40, 2056, 4100, "bf16", "linear_rows_bf16"), (40, 1029, 4100, "f32", "linear_rows_f32"),
+    (40, 333, 100, "bf16", "linear_rows_bf16"),
     (1000, 72, 1000, "bf16", "linear_tile_bf16/64"), (1000, 32, 1000, "f32", "linear_tile_f32/64"),
     (1000, 136, 4000, "bf16", "linear_tile_bf16/128deep"), (2000, 44, 2000, "f32", "linear_tile_f32/128deep"),
     (2000, 72, 4000, "bf16", "linear_tile_bf16/128"), (4090, 72, 4088, "bf16", "linear_tile_bf16/256"),
