@@ -30,8 +30,10 @@ struct RowsAttn {
     static constexpr int BK = 32;
     static constexpr int OUT = VC * C;                                // 16x16 output blocks
     // A tile takes a quarter of the row's bytes in registers: rows to 256 bytes
-    // leave room for two waves on a SIMD, each with two tiles.
-    static constexpr int RB = DP * (int)sizeof(T), NBUF = RB <= 512 ? 2 : 1, OCC = RB <= 256 ? 2 : 1, NW = 4;
+    // leave room for two waves on a SIMD, each with two tiles.  Two tiles of
+    // 256 bf16 leave no register (16x4096 keys: 115 us, 109 with one); of 128
+    // fp32, without the permutes, they pay (115, 122 with one).
+    static constexpr int RB = DP * (int)sizeof(T), NBUF = DP <= 128 ? 2 : 1, OCC = RB <= 256 ? 2 : 1, NW = 4;
     u32x4 k[2][KS];
     u32x4 v[8][VC];
 
@@ -70,7 +72,7 @@ __device__ __forceinline__ int by_length(const AttnArgs& a, int i, int lane) {
     const int mine = lane < a.batch ? a.kv_lens[lane] : 0;
     int rank = 0;
     for (int j = 0; j < a.batch; ++j) {
-        const int other = __shfl(mine, j, 64);
+        const int other = __builtin_amdgcn_readlane(mine, j);
         rank += other > mine || (other == mine && j < lane);
     }
     const uint64_t hit = __ballot(lane < a.batch && rank == i);
