@@ -388,13 +388,17 @@ AttnPlan plan_attention(int32_t dtype, const AttnArgs& a) {
     p.kernel = a.rows <= (dtype == CONV_DTYPE_F32 ? 32 : 16)       ? ATTN_ROWS
                : near ? ATTN_TILE_128
                       : ATTN_ANY;
+    // Heads beyond 128 leave room for one workgroup on a CU in either size:
+    // 2500 causal rows of 16 heads of 256 over 4 (316 tiles of 128) take 130 us
+    // in them and 147 in tiles of 64, 1300 rows (164 tiles) 57.4 and 52.5.
+    const int64_t cus = device_cu_count();
     if (p.kernel == ATTN_TILE_128 && !(dtype == CONV_DTYPE_F32 && a.d > 128) &&
-        (int64_t)a.batch * a.heads_kv * ((a.rows + 127) / 128) < 2 * device_cu_count())
+        (int64_t)a.batch * a.heads_kv * ((a.rows + 127) / 128) < (a.d > 128 ? cus * 3 / 4 : cus * 2))
         p.kernel = ATTN_TILE_64;
     const int tile = p.kernel == ATTN_ROWS ? 16 : p.kernel == ATTN_TILE_128 ? 128 : 64;
     p.row_tiles = (a.rows + tile - 1) / tile;
     // Few row tiles leave compute units without work: the keys are then split.
-    const int64_t tiles = (int64_t)a.batch * a.heads_kv * p.row_tiles, cus = device_cu_count();
+    const int64_t tiles = (int64_t)a.batch * a.heads_kv * p.row_tiles;
     // Workgroups wanted, and keys for each at least.  The partial results of
     // many rows cost as much as a few hundred keys of bf16: 1000 causal rows of
     // 16 heads of 128 over 4 take 22.8 us undivided, 27.5 in two.

@@ -114,6 +114,16 @@ def test_enough_rows_for_whole_tiles(dtype, d, c):
     assert _check(2, 210, 210, 256, 128, d, dtype, kv_lens=[210, 77], q_lens=[210, 77], **c) == 0
 
 
+@pytest.mark.parametrize("d,batch,kv_len,c", [
+    (256, 2, 140, dict(causal=True)), (200, 2, 333, dict(softcap=30.0, slopes=True)), (256, 1, 1100, dict(window=300)),
+])
+def test_wide_heads(d, batch, kv_len, c):
+    """Heads beyond 128 in 128-row tiles, from 192 of them on, and in 64-row tiles below; long keys are divided."""
+    for heads in (50, 47):
+        _check(batch, 140 if batch == 2 else 500, kv_len, heads, heads, d, "bf16",
+               kv_lens=None if batch == 1 else [kv_len, kv_len - 131], **c)
+
+
 def test_unseen_garbage_in_whole_tiles():
     def spoil(k, v):
         v[0, 205, 3, 5] = float("inf")     # seen by the last rows alone
