@@ -399,11 +399,15 @@ AttnPlan plan_attention(int32_t dtype, const AttnArgs& a) {
     p.row_tiles = (a.rows + tile - 1) / tile;
     // Few row tiles leave compute units without work: the keys are then split.
     const int64_t tiles = (int64_t)a.batch * a.heads_kv * p.row_tiles;
-    // Workgroups wanted, and keys for each at least.  The partial results of
-    // many rows cost as much as a few hundred keys of bf16: 1000 causal rows of
-    // 16 heads of 128 over 4 take 22.8 us undivided, 27.5 in two.
-    int64_t want = p.kernel == ATTN_TILE_64 ? cus : 2 * cus;
-    int64_t keys = dtype != CONV_DTYPE_F32 && tiles * 2 >= cus ? 1024 : 256;
+    // Workgroups wanted, and keys for each at least.  Two a unit even out rows
+    // of different lengths (5322 causal rows of 4 heads of 64: 77.6 us with
+    // one, 51.7 with two).  The partial results of many rows cost as much as a
+    // few hundred keys: 1000 causal rows of 16 heads of 128 over 4 take 22.8 us
+    // undivided, 27.5 in two; 538 of 12 fp32 heads of 128 48.6 us in parts of
+    // 256 keys, 39.2 of 512.
+    const bool f32 = dtype == CONV_DTYPE_F32;
+    int64_t want = 2 * cus;
+    int64_t keys = f32 ? 512 : tiles * 2 >= cus ? 1024 : 256;
     if (p.kernel == ATTN_ROWS) {
         // Two workgroups fit on a unit (one where a row of K has more than 256
         // bytes); a third per unit evens out sequences of different lengths.
@@ -411,7 +415,9 @@ AttnPlan plan_attention(int32_t dtype, const AttnArgs& a) {
         want = big ? cus : a.batch > 1 ? 3 * cus : 2 * cus;
         keys = tiles >= cus ? 1024 : tiles * 2 >= cus ? 512 : 128;
     }
-    int64_t s = tiles < want ? (want + tiles - 1) / tiles : 1;
+    // Of wide fp32 rows one workgroup fits on a unit: the nearest, not the next
+    // number of parts (252 tiles of 128: 108 us in two, 116 in three).
+    int64_t s = tiles < want ? (want + (f32 && p.kernel != ATTN_ROWS ? tiles / 2 : tiles - 1)) / tiles : 1;
     const int64_t most = ((int64_t)a.kv_len + keys - 1) / keys;
     if (s > most) s = most;
     if (s > ATTN_MAX_SPLITS) s = ATTN_MAX_SPLITS;
