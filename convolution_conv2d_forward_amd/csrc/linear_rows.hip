@@ -1,4 +1,5 @@
-// y = act(x w^T + bias) + residual for few rows of x: bound by the bytes of w.
+// y = act(x w^T + bias) + residual for few rows of x, bound by the bytes of w, and
+// for few tiles of a long k, bound by the latency of its units.
 #include "linear_common.h"
 
 namespace conv2d {
