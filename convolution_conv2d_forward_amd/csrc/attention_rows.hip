@@ -9,7 +9,7 @@ namespace {
 
 // 16 of the rows (query i, head of the group) that share a key head
 // per workgroup.  It is bound by the bytes of K and V, so every wave reads
-// tiles of 32 keys of its own, straight from memory into the operands of the
+// tiles of 32 keys (or 16) of its own, straight from memory into the operands of the
 // matrix cores, with the next tile's loads in flight, and no LDS or barrier
 // stands between; the waves' results meet in LDS once, at the end, and the
 // splits' in the workspace.
@@ -27,22 +27,24 @@ struct RowsAttn {
     static constexpr int C = Vec<T>::chunk;
     static constexpr int KS = DP * (int)sizeof(T) / 64;               // 64-byte product steps over a row
     static constexpr int VC = (DP / C + 15) / 16;                     // 16-chunk groups of a row of V
-    static constexpr int BK = 32;
+    // Keys of a tile: rows of 1024 bytes spilled at 32 (8x4096 keys of 8 heads of
+    // 256 fp32: 157 us, 130 at 16; a few keys: 18.4 and 12.5).
+    static constexpr int BK = DP * (int)sizeof(T) > 512 ? 16 : 32, NT = BK / 16, NJ = BK / 4;
     static constexpr int OUT = VC * C;                                // 16x16 output blocks
     // A tile takes a quarter of the row's bytes in registers: rows to 256 bytes
     // leave room for two waves on a SIMD, each with two tiles.  Two tiles of
     // 256 bf16 leave no register (16x4096 keys: 115 us, 109 with one); of 128
     // fp32, without the permutes, they pay (115, 122 with one).
     static constexpr int RB = DP * (int)sizeof(T), NBUF = DP <= 128 ? 2 : 1, OCC = RB <= 256 ? 2 : 1, NW = 4;
-    u32x4 k[2][KS];
-    u32x4 v[8][VC];
+    u32x4 k[NT][KS];
+    u32x4 v[NJ][VC];
 
     // A tile's loads.  Keys from nk on repeat the last one.
     __device__ __forceinline__ void load(const T* kp, const T* vp, int64_t ks, int64_t vs, int k0, int nk, int d,
                                          int lane) {
         const int r = lane & 15, g = lane >> 4;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < NT; ++t) {
             const int key = sizeof(T) == 2 ? 8 * (r >> 2) + 4 * t + (r & 3) : 16 * t + r;
             const T* p = kp + min(k0 + key, nk - 1) * ks;
 #pragma unroll
@@ -53,7 +55,7 @@ struct RowsAttn {
             }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < NJ; ++j) {
             const int key = sizeof(T) == 2 ? 8 * g + j : 16 * (j >> 2) + 4 * g + (j & 3);
             const T* p = vp + min(k0 + key, nk - 1) * vs;
 #pragma unroll
@@ -82,7 +84,7 @@ __device__ __forceinline__ int by_length(const AttnArgs& a, int i, int lane) {
 template <typename T, int DP>
 __global__ __launch_bounds__((64 * RowsAttn<T, DP>::NW), (RowsAttn<T, DP>::OCC)) void attention_rows(AttnArgs a) {
     typedef RowsAttn<T, DP> R;
-    constexpr int C = R::C, KS = R::KS, VC = R::VC, NW = R::NW, BK = R::BK, OUT = R::OUT;
+    constexpr int C = R::C, KS = R::KS, VC = R::VC, NW = R::NW, BK = R::BK, NT = R::NT, NJ = R::NJ, OUT = R::OUT;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
     // Sequence, key head, split, row tile: with the longest sequences first,
@@ -144,26 +146,26 @@ __global__ __launch_bounds__((64 * RowsAttn<T, DP>::NW), (RowsAttn<T, DP>::OCC))
         bool bad = false;
         if (!whole) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < NJ; ++j)
 #pragma unroll
                 for (int c = 0; c < VC; ++c) bad |= has_bad<T>(f.v[j][c]);
             bad = __ballot(bad) != 0;
         }
         if (bad) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < NJ; ++j)
 #pragma unroll
                 for (int c = 0; c < VC; ++c) clean_chunk<T>(f.v[j][c]);
         }
-        float p[2][4];
-        f32x4 s[2] = {};
+        float p[NT][4];
+        f32x4 s[NT] = {};
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < KS; ++i) s[t] = mfma_step<T>(f.k[t][i], fq[i], s[t]);
         float top = -INFINITY;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int key = k0 + (sizeof(T) == 2 ? 8 * g + 4 * t + i : 16 * t + 4 * g + i);
@@ -181,7 +183,7 @@ __global__ __launch_bounds__((64 * RowsAttn<T, DP>::NW), (RowsAttn<T, DP>::OCC))
         m_run = m_new;
         l_run *= fade;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 p[t][i] = __builtin_amdgcn_exp2f(s[t][i] - base);
@@ -211,13 +213,13 @@ __global__ __launch_bounds__((64 * RowsAttn<T, DP>::NW), (RowsAttn<T, DP>::OCC))
 #pragma unroll
                 for (int e = 0; e < C; ++e)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
+                    for (int j = 0; j < NJ; ++j)
                         o[c * C + e] = __builtin_amdgcn_mfma_f32_16x16x4f32(
                             __builtin_bit_cast(f32x4, f.v[j][c])[e], p[j >> 2][j & 3], o[c * C + e], 0, 0, 0);
         }
         if (bad) {
             // Output block (c, e) of lane l has rows 16 c C + (4 (l / 16) + i) C + e of V^T.
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < NJ; ++j)
 #pragma unroll 1
                 for (int gg = 0; gg < 4; ++gg) {
                     const int key = k0 + (sizeof(T) == 2 ? 8 * gg + j : 16 * (j >> 2) + 4 * gg + (j & 3));
