@@ -179,7 +179,10 @@ __global__ __launch_bounds__(256, (TileAttn<T, DP, KW>::OCC)) void attention_til
     const int first = __builtin_amdgcn_readfirstlane(t0 + (int)((int64_t)tn * split / a.splits));
     const int last = __builtin_amdgcn_readfirstlane(t0 + (int)((int64_t)tn * (split + 1) / a.splits));
 
-    // Q as the products' second operand; a negative scale goes into its signs.
+    // Q as the products' second operand; a negative scale goes into its signs,
+    // and one of zero makes it zero: a masked score, -inf, is multiplied by the
+    // scale later (PLAIN), which has to leave it -inf.
+    const bool flat = a.scale == 0.0f;
     const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
     u32x4 fq[KS];
     {
@@ -188,11 +191,11 @@ __global__ __launch_bounds__(256, (TileAttn<T, DP, KW>::OCC)) void attention_til
         for (int s = 0; s < KS; ++s) {
             const int e = (2 * s + g) * C::C;
             fq[s] = u32x4{0, 0, 0, 0};
-            if (live && e < a.d) fq[s] = *(const u32x4*)(qp + e);
+            if (live && e < a.d && !flat) fq[s] = *(const u32x4*)(qp + e);
             if (a.scale < 0.0f) fq[s] ^= HALF ? 0x80008000u : 0x80000000u;
         }
     }
-    const float scale = sign * a.scale * kLog2e;                     // scores in units of log 2
+    const float scale = flat ? 1.0f : sign * a.scale * kLog2e;       // scores in units of log 2
     const float cap = a.softcap * kLog2e;
     const float tscale = CAP ? fabsf(a.scale) / a.softcap * (HALF ? 2.0f * kLog2e : 1.0f) : 0.0f;
     const float slope = SLOPE && live ? a.slopes[hq] * kLog2e : 0.0f;
