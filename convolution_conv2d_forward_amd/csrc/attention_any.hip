@@ -135,14 +135,16 @@ __global__ __launch_bounds__(256) void attention_any(AttnArgs a) {
                 const u32x4 fk = *(const u32x4*)(lk + (16 * t + n) * LROW + (ks * 4 + g) * C);
                 s[t] = mfma_step<T>(fk, fq[ks], s[t]);
             }
-        float m_new = m_run;
+        float m_new = m_run, sc[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sc[i] = s[i >> 2][i & 3];
+        scores<T>(sp, sc);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int key = k0 + 16 * t + 4 * g + i;
-                float x = s[t][i] * sp.scale;
-                if (sp.cap > 0.0f) x = sp.cap * score_tanh<T>(x);
+                float x = sc[4 * t + i];
                 if (a.slopes) x -= slope * fabsf((float)(pos - key));
                 if (!whole) x = key >= lo && key < hi ? x : -INFINITY;
                 s[t][i] = x;

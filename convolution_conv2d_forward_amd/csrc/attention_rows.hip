@@ -163,14 +163,16 @@ __global__ __launch_bounds__((64 * RowsAttn<T, DP>::NW), (RowsAttn<T, DP>::OCC))
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < KS; ++i) s[t] = mfma_step<T>(f.k[t][i], fq[i], s[t]);
-        float top = -INFINITY;
+        float top = -INFINITY, sc[4 * NT];
+#pragma unroll
+        for (int i = 0; i < 4 * NT; ++i) sc[i] = s[i >> 2][i & 3];
+        scores<T>(sp, sc);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int key = k0 + (sizeof(T) == 2 ? 8 * g + 4 * t + i : 16 * t + 4 * g + i);
-                float x = s[t][i] * sp.scale;
-                if (sp.cap > 0.0f) x = sp.cap * score_tanh<T>(x);
+                float x = sc[4 * t + i];
                 if (a.slopes) x -= slope * fabsf((float)(pos - key));
                 if (!whole) x = key >= lo && key < hi ? x : -INFINITY;
                 s[t][i] = x;

@@ -111,15 +111,14 @@ struct TileAttn {
     }
 };
 
-template <typename T, int DP, int KW, bool CAP, bool SLOPE>
+template <typename T, int DP, int KW, int CAP, bool SLOPE>
 __global__ __launch_bounds__(256, (TileAttn<T, DP, KW>::OCC)) void attention_tile(AttnArgs a) {
     typedef TileAttn<T, DP, KW> C;
     constexpr bool HALF = C::HALF;
     constexpr int BK = C::BK, TK = C::TK, CPR = C::CPR, KS = C::KS, DT = C::DT, CP = C::CP;
     // How a score x follows from what its register holds, u: x = u itself; or
-    // PLAIN, x = scale u; or TURNED (bf16, capped), x = cap (1 - 2 u), where
-    // u = 1 / (exp(2 t) + 1) gives tanh t = 1 - 2 u.
-    constexpr bool PLAIN = !CAP && !SLOPE, TURNED = CAP && !SLOPE && HALF;
+    // PLAIN, x = scale u; or TURNED, x = cap (1 - 2 u).
+    constexpr bool PLAIN = !CAP && !SLOPE, TURNED = CAP == kCapTurned && !SLOPE;
     __shared__ __align__(1024) u32x4 lds[C::S * C::STAGE];
     __shared__ int lrange[4][4];
     // The last even and odd tile that held infinities or NaN: a wave may reach
@@ -196,8 +195,10 @@ __global__ __launch_bounds__(256, (TileAttn<T, DP, KW>::OCC)) void attention_til
         }
     }
     const float scale = flat ? 1.0f : sign * a.scale * kLog2e;       // scores in units of log 2
-    const float cap = a.softcap * kLog2e;
-    const float tscale = CAP ? fabsf(a.scale) / a.softcap * (HALF ? 2.0f * kLog2e : 1.0f) : 0.0f;
+    const float cap = CAP == kCapTurned ? a.softcap * kLog2e : a.softcap;
+    const float tscale = CAP == kCapTurned ? fminf(fabsf(a.scale) / a.softcap * (2.0f * kLog2e), FLT_MAX)
+                         : CAP             ? cap_scale(fabsf(a.scale), a.softcap)
+                                           : 0.0f;
     const float slope = SLOPE && live ? a.slopes[hq] * kLog2e : 0.0f;
     const int pos = sl.nk - sl.nq + qi;
 
@@ -274,11 +275,11 @@ __global__ __launch_bounds__(256, (TileAttn<T, DP, KW>::OCC)) void attention_til
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     float x = s[t][i];
-                    if (CAP && HALF) {
-                        x = __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * tscale) + 1.0f);
+                    if (CAP == kCapTurned) {
+                        x = turned(x * tscale);
                         if (SLOPE) x = cap - 2.0f * cap * x;
                     } else if (CAP) {
-                        x = cap * tanhf(x * tscale);
+                        x = cap * score_tanh<T>(x * tscale) * kLog2e;
                     } else {
                         x *= scale;
                     }
@@ -424,14 +425,18 @@ __global__ __launch_bounds__(256, (TileAttn<T, DP, KW>::OCC)) void attention_til
 template <typename T, int DP, int KW>
 hipError_t run(const AttnArgs& a, hipStream_t s) {
     const dim3 grid((uint32_t)((int64_t)a.batch * a.heads_kv * a.row_tiles * a.splits)), block(256);
-    if (a.softcap > 0.0f && a.slopes)
-        attention_tile<T, DP, KW, true, true><<<grid, block, 0, s>>>(a);
-    else if (a.softcap > 0.0f)
-        attention_tile<T, DP, KW, true, false><<<grid, block, 0, s>>>(a);
-    else if (a.slopes)
-        attention_tile<T, DP, KW, false, true><<<grid, block, 0, s>>>(a);
-    else
-        attention_tile<T, DP, KW, false, false><<<grid, block, 0, s>>>(a);
+    const auto launch = [&](auto cap) {
+        if (a.slopes)
+            attention_tile<T, DP, KW, cap(), true><<<grid, block, 0, s>>>(a);
+        else
+            attention_tile<T, DP, KW, cap(), false><<<grid, block, 0, s>>>(a);
+    };
+    if (a.softcap == 0.0f)
+        launch(std::integral_constant<int, kCapNone>{});
+    else if (sizeof(T) == 4 || a.softcap > kMostTurned)
+        launch(std::integral_constant<int, kCapAny>{});
+    else if constexpr (sizeof(T) == 2)
+        launch(std::integral_constant<int, kCapTurned>{});
     return hipGetLastError();
 }
 

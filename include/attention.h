@@ -22,7 +22,9 @@
  * UNSUPPORTED).  Sums, norms, angles and softmax statistics are held in fp32
  * or more for both; a bf16 result is rounded once, to nearest even (in
  * attention_forward the softmax weights are rounded to bf16 before they meet
- * bf16 values on the matrix cores).  Strides count elements.
+ * bf16 values on the matrix cores, and a capped score may be off by softcap *
+ * 2^-21 up to a softcap of 512, by 2^-21 of itself beyond).  Strides count
+ * elements.
  */
 #ifndef ATTENTION_MI355X_H
 #define ATTENTION_MI355X_H

@@ -1,9 +1,11 @@
-"""GPU: attention_forward where scales leave the usual range: a scale of zero
-weighs all seen keys alike."""
+"""GPU: attention_forward where scales and caps leave the usual range: a scale of
+zero, which weighs all seen keys alike, and caps far above every score."""
+import math
+
 import pytest
 import torch
 
-from attention_reference import assert_within, attention64
+from attention_reference import FN, ROUND, U32, assert_within, attention64, seen
 from test_gpu_attention import _call, _inputs
 
 pytestmark = pytest.mark.gpu
@@ -25,3 +27,60 @@ def test_zero_scale_is_the_mean_of_the_seen_values(scale, kw, q_len, dtype, d):
     got = _call(q.cuda(), k.cuda(), v.cuda(), {**c, "scale": scale}, **lens)
     want, tol = attention64(torch.zeros_like(q), k, v, c, None, lens.get("kv_lens"), None, lens.get("docs"))
     assert_within(got, want, tol, f"{scale} {kw}")
+
+
+def _capped64(q, k, v, cap, slopes, dtype):
+    """Causal attention with capped scores and a bound on its error in which a
+    score's cap costs 2^-21 of the score, whatever the cap."""
+    b, q_len, hq, d = q.shape
+    kv_len, group = k.shape[1], hq // k.shape[2]
+    see = seen(q_len, kv_len, q_len, kv_len, causal=True, window=0, prefix=None, docs=None)
+    dist = (kv_len - q_len + torch.arange(q_len)[:, None] - torch.arange(kv_len)[None, :]).abs().double()
+    out = torch.zeros(q.shape, dtype=torch.float64)
+    tol = torch.zeros_like(out)
+    for n in range(b):
+        for h in range(hq):
+            qq, kk, vv = q[n, :, h].double(), k[n, :, h // group].double(), v[n, :, h // group].double()
+            s = cap * torch.tanh(qq @ kk.T * d ** -0.5 / cap)
+            # The product's terms, the scale's and the cap's roundings, the function.
+            err = (d + 8) * U32 * d ** -0.5 * (qq.abs() @ kk.abs().T) + FN * s.abs()
+            if slopes is not None:
+                bias = slopes[h].double() * dist
+                s, err = s - bias, err + 4 * U32 * bias
+            err = err + 4 * U32 * s.abs()
+            w = torch.softmax(torch.where(see, s, -math.inf), 1)
+            size = w @ vv.abs()
+            e = torch.where(see & (w > 2.0 ** -20), err, 0.0).amax(1, keepdim=True)
+            rel = 2 * e + 2 * FN + 2 * kv_len * U32 + (ROUND[dtype] if dtype == "bf16" else 0.0)
+            out[n, :, h] = w @ vv
+            tol[n, :, h] = size * rel + ROUND[dtype] * out[n, :, h].abs() + 2.0 ** -20 * kv_len * U32 + 1e-30
+    return out, tol
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("q_len", [1, 12, 90])
+@pytest.mark.parametrize("with_slopes", [False, True])
+@pytest.mark.parametrize("cap", [600.0, 1e4, 1e6, 1e9, 1e30, 3e38])
+def test_large_caps(cap, with_slopes, q_len, dtype, d):
+    q, k, v = _inputs(2, q_len, 200, 4, 2, d, dtype, 7)
+    slopes = torch.exp2(-2.0 * torch.arange(1, 5)).float() if with_slopes else None
+    got = _call(q.cuda(), k.cuda(), v.cuda(), {"dtype": dtype, "causal": True, "softcap": cap}, slopes=slopes)
+    want, tol = _capped64(q, k, v, cap, slopes, dtype)
+    assert_within(got, want, tol, f"cap {cap}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("q_len", [1, 90])
+@pytest.mark.parametrize("with_slopes", [False, True])
+@pytest.mark.parametrize("cap", [1e-3, 1e-30, 1e-42])
+def test_small_caps(cap, with_slopes, q_len, dtype):
+    """Scores of at most the cap, also where the quotient scale / cap passes the
+    largest fp32 number; one key's score is zero.  The bound lets the function
+    be off by 2^-21 of the cap."""
+    q, k, v = _inputs(1, q_len, 150, 4, 2, 64, dtype, 8)
+    k[0, 3] = 0
+    slopes = torch.exp2(-2.0 * torch.arange(1, 5)).float() if with_slopes else None
+    c = {"dtype": dtype, "causal": True, "softcap": cap}
+    got = _call(q.cuda(), k.cuda(), v.cuda(), c, slopes=slopes)
+    want, tol = attention64(q, k, v, c, slopes=slopes)
+    assert_within(got, want, tol, f"cap {cap}")
