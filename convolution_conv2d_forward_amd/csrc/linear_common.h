@@ -53,8 +53,8 @@ __device__ __forceinline__ f32x16 mfma32_step<float>(u32x4 a, u32x4 b, f32x16 c)
 // and wait for its instructions.
 enum { kActNone, kActPiecewise, kActSilu, kActGelu, kActGeluTanh };
 
-// The activation of N values.  tanh(u) through 1 - 2 / (exp(2u) + 1) keeps its
-// absolute error near 2^-24, which is what (1 + tanh) is added to.
+// The activation of N values.  v (1 + tanh u) / 2 is v / (1 + exp(-2u)): nothing
+// cancels in it, so the tail keeps its relative accuracy and +inf stays.
 template <int KIND, int N>
 __device__ __forceinline__ void linear_act(const LinearArgs& a, float* v) {
 #pragma unroll
@@ -71,7 +71,7 @@ __device__ __forceinline__ void linear_act(const LinearArgs& a, float* v) {
             v[i] = 0.5f * x * (1.0f + erff(x * 0.70710678118654752440f));
         } else if constexpr (KIND == kActGeluTanh) {
             const float u = 0.79788456080286535588f * (x + 0.044715f * x * x * x);
-            v[i] = x - x / (1.0f + __expf(2.0f * u));
+            v[i] = x / (1.0f + __expf(-2.0f * u));
         }
     }
 }
