@@ -53,9 +53,22 @@ __device__ __forceinline__ f32x16 mfma32_step<float>(u32x4 a, u32x4 b, f32x16 c)
 // and wait for its instructions.
 enum { kActNone, kActPiecewise, kActSilu, kActGelu, kActGeluTanh };
 
+// exp for results of type T.  The hardware's takes x log2(e) rounded, which is
+// off by some 2^-24 x: bf16 does not show that, for fp32 what the rounding left,
+// `low`, goes onto the result.  (expf has the same correction, which this
+// library's -ffp-contract=fast undoes: it fuses a product into a difference
+// that relies on the product's rounding.)
+template <typename T>
+__device__ __forceinline__ float act_exp(float x) {
+    const float t = x * kLog2e, r = __builtin_amdgcn_exp2f(t);
+    if (sizeof(T) == 2) return r;
+    const float low = __builtin_fmaf(x, 1.92596299112661746887e-8f, __builtin_fmaf(x, kLog2e, -t));
+    return fabsf(t) < 128.0f ? __builtin_fmaf(r, low * 0.69314718055994530942f, r) : r;
+}
+
 // The activation of N values.  v (1 + tanh u) / 2 is v / (1 + exp(-2u)): nothing
 // cancels in it, so the tail keeps its relative accuracy and +inf stays.
-template <int KIND, int N>
+template <typename T, int KIND, int N>
 __device__ __forceinline__ void linear_act(const LinearArgs& a, float* v) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -66,12 +79,12 @@ __device__ __forceinline__ void linear_act(const LinearArgs& a, float* v) {
             else   // RELU (act_a = 0) and LEAKY_RELU; NaN stays
                 v[i] = x > 0.0f ? x : a.act_a == 0.0f ? (x != x ? x : 0.0f) : a.act_a * x;
         } else if constexpr (KIND == kActSilu) {
-            v[i] = x / (1.0f + __expf(-x));
+            v[i] = x / (1.0f + act_exp<T>(-x));
         } else if constexpr (KIND == kActGelu) {
             v[i] = 0.5f * x * (1.0f + erff(x * 0.70710678118654752440f));
         } else if constexpr (KIND == kActGeluTanh) {
             const float u = 0.79788456080286535588f * (x + 0.044715f * x * x * x);
-            v[i] = x / (1.0f + __expf(-2.0f * u));
+            v[i] = x / (1.0f + act_exp<T>(-2.0f * u));
         }
     }
 }

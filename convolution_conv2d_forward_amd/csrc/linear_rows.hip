@@ -7,14 +7,14 @@ namespace conv2d {
 namespace {
 
 // The activation, its kind at run time: for the few outputs of a thread here.
-template <int N>
+template <typename T, int N>
 __device__ __forceinline__ void linear_act_any(const LinearArgs& a, float* v) {
     switch (a.act) {
     case CONV_ACT_NONE: break;
-    case LINEAR_ACT_SILU: linear_act<kActSilu, N>(a, v); break;
-    case LINEAR_ACT_GELU: linear_act<kActGelu, N>(a, v); break;
-    case LINEAR_ACT_GELU_TANH: linear_act<kActGeluTanh, N>(a, v); break;
-    default: linear_act<kActPiecewise, N>(a, v);
+    case LINEAR_ACT_SILU: linear_act<T, kActSilu, N>(a, v); break;
+    case LINEAR_ACT_GELU: linear_act<T, kActGelu, N>(a, v); break;
+    case LINEAR_ACT_GELU_TANH: linear_act<T, kActGeluTanh, N>(a, v); break;
+    default: linear_act<T, kActPiecewise, N>(a, v);
     }
 }
 
@@ -39,7 +39,7 @@ __device__ __forceinline__ void rows_store(const LinearArgs& a, const f32x4 (&ac
         for (int i = 1; i < NW; ++i) v += red[(i * NT * MT + t) * 64 + lane];
         if (a.vec_out) {
             if (a.bias) v += *(const f32x4*)(a.bias + n);
-            linear_act_any<4>(a, (float*)&v);
+            linear_act_any<T, 4>(a, (float*)&v);
             if (res) v += to_f32(*(const typename Vec<T>::v4*)res);
             *(typename Vec<T>::v4*)y = from_f32<T>(v);
             continue;
@@ -47,7 +47,7 @@ __device__ __forceinline__ void rows_store(const LinearArgs& a, const f32x4 (&ac
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (a.bias && n + i < a.n) v[i] += a.bias[n + i];
-        linear_act_any<4>(a, (float*)&v);
+        linear_act_any<T, 4>(a, (float*)&v);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (n + i < a.n) y[i] = from_f32<T>(v[i] + (res ? to_f32(res[i]) : 0.0f));

@@ -108,7 +108,7 @@ __device__ __forceinline__ void tile_store(const LinearArgs& a, const f32x16 (&a
                 __builtin_memcpy(v + 4, &os[at(r0 + 16 * h, 2 * c0 + 1)], 16);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] += b[e];
-                linear_act<ACT, 8>(a, v);
+                linear_act<T, ACT, 8>(a, v);
                 const f32x8 r = __builtin_convertvector(res[j][h], f32x8);
                 f32x8 o;
 #pragma unroll

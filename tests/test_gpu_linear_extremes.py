@@ -51,3 +51,13 @@ def test_gelu_tanh_keeps_its_relative_accuracy(m, dtype):
     rel = 2 * u.abs() * 8 * U32 + FN + 8 * U32 + ROUND[dtype]
     over = (y - want).abs() / want.abs() / rel
     assert (over <= 1).all(), (float(v[over.argmax()]), float(over.max()))
+
+
+@pytest.mark.parametrize("m", [9, 147, 300])
+def test_silu_keeps_its_relative_accuracy(m):
+    """fp32: v / (1 + exp(-v)), the exponential and the quotient off by 2^-21
+    together, down to -85, where it is 1e-35."""
+    v, y = _apply([-0.01 * 1.064 ** i for i in range(147)], "silu", "f32", m)
+    want = v / (1 + torch.exp(-v))
+    over = (y - want).abs() / want.abs() / (FN + 4 * U32)
+    assert (over <= 1).all(), (float(v[over.argmax()]), float(over.max()))
