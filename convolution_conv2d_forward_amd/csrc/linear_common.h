@@ -66,8 +66,25 @@ __device__ __forceinline__ float act_exp(float x) {
     return fabsf(t) < 128.0f ? __builtin_fmaf(r, low * 0.69314718055994530942f, r) : r;
 }
 
-// The activation of N values.  v (1 + tanh u) / 2 is v / (1 + exp(-2u)): nothing
-// cancels in it, so the tail keeps its relative accuracy and +inf stays.
+// x (1 + erf(x / sqrt 2)) / 2 as x erfc(-x / sqrt 2) / 2.  With z = |x| / sqrt 2
+// and t = 1 / (1 + 0.3 z), erfc(z) exp(z^2) is t times a polynomial of t fitted
+// to 2e-8 relative for z up to 9.5, where fp32's smallest number lies; 5e-7 as
+// evaluated here.  (4096x1024->4096 bf16 47 us, with erfcf 59.)
+template <typename T>
+__device__ __forceinline__ float gelu_erf(float x) {
+    const float c[9] = {0.169189617f, 0.170691982f, 0.148482114f, 0.214437470f, -0.0936339349f,
+                        0.546398759f, -0.511229634f, 0.485097945f, -0.129434377f};
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.3f * 0.70710678118654752440f * fabsf(x));
+    float p = c[8];
+#pragma unroll
+    for (int i = 7; i >= 0; --i) p = __builtin_fmaf(p, t, c[i]);
+    const float q = p * t * act_exp<T>(-0.5f * x * x);
+    return 0.5f * x * (x > 0.0f ? 2.0f - q : q);
+}
+
+// The activation of N values.  v (1 + tanh u) / 2 is v / (1 + exp(-2u)), and
+// v (1 + erf z) / 2 is v erfc(-z) / 2: nothing cancels in them, so the tails
+// keep their relative accuracy and +inf stays.
 template <typename T, int KIND, int N>
 __device__ __forceinline__ void linear_act(const LinearArgs& a, float* v) {
 #pragma unroll
@@ -81,7 +98,7 @@ __device__ __forceinline__ void linear_act(const LinearArgs& a, float* v) {
         } else if constexpr (KIND == kActSilu) {
             v[i] = x / (1.0f + act_exp<T>(-x));
         } else if constexpr (KIND == kActGelu) {
-            v[i] = 0.5f * x * (1.0f + erff(x * 0.70710678118654752440f));
+            v[i] = gelu_erf<T>(x);
         } else if constexpr (KIND == kActGeluTanh) {
             const float u = 0.79788456080286535588f * (x + 0.044715f * x * x * x);
             v[i] = x / (1.0f + act_exp<T>(-2.0f * u));

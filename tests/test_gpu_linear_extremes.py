@@ -61,3 +61,15 @@ def test_silu_keeps_its_relative_accuracy(m):
     want = v / (1 + torch.exp(-v))
     over = (y - want).abs() / want.abs() / (FN + 4 * U32)
     assert (over <= 1).all(), (float(v[over.argmax()]), float(over.max()))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m", [9, 147, 300])
+def test_gelu_keeps_its_relative_accuracy(m, dtype):
+    """v erfc(-v / sqrt 2) / 2: the argument z is off by 2 roundings, which
+    erfc multiplies by up to 2 z^2 + 1; the function by 2^-21."""
+    v, y = _apply(TAIL, "gelu", dtype, m)
+    want = 0.5 * v * torch.special.erfc(-v / math.sqrt(2))
+    rel = (v * v + 1) * 2 * U32 + FN + 8 * U32 + ROUND[dtype]
+    over = (y - want).abs() / want.abs() / rel
+    assert (over <= 1).all(), (float(v[over.argmax()]), float(over.max()))
