@@ -429,6 +429,26 @@ AttnPlan plan_attention(int32_t dtype, const AttnArgs& a) {
 }
 
 hipError_t launch_attention(int32_t dtype, const AttnPlan& p, const AttnArgs& a, hipStream_t s) {
+    const int64_t most = most_workgroups(256) / sequence_workgroups(a, p);
+    if (a.batch > most) {
+        // So many workgroups that the keys are not divided: no workspace.
+        const int64_t es = dtype == CONV_DTYPE_F32 ? 4 : 2;
+        for (int64_t b = 0; b < a.batch; b += most) {
+            AttnArgs c = a;
+            c.batch = (int32_t)(a.batch - b < most ? a.batch - b : most);
+            c.q = (const char*)a.q + b * a.q_s[0] * es;
+            c.k = (const char*)a.k + b * a.k_s[0] * es;
+            c.v = (const char*)a.v + b * a.v_s[0] * es;
+            c.out = (char*)a.out + b * a.o_s[0] * es;
+            if (a.q_lens) c.q_lens = a.q_lens + b;
+            if (a.kv_lens) c.kv_lens = a.kv_lens + b;
+            if (a.prefix_lens) c.prefix_lens = a.prefix_lens + b;
+            if (a.doc_offsets) c.doc_offsets = a.doc_offsets + b * (a.n_docs + 1);
+            const hipError_t e = launch_attention(dtype, p, c, s);
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
+    }
     const bool f32 = dtype == CONV_DTYPE_F32;
     const int rows = p.kernel == ATTN_TILE_128 ? 128 : 64;
     hipError_t e;

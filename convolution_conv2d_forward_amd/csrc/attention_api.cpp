@@ -149,10 +149,10 @@ conv_status_t check_attn_sizes(const attention_params_t& p, int64_t batch, int64
     return CONV_OK;
 }
 
-// The plan's grid.
+// The plan's grid: sequences may be divided over launches, one may not.
 conv_status_t check_attn_grid(const AttnArgs& a, const AttnPlan& p) {
-    if ((int64_t)a.batch * a.heads_kv * p.row_tiles * p.splits > kMaxRows)
-        return fail(CONV_ERR_UNSUPPORTED, "grid beyond 2^31 workgroups");
+    if (sequence_workgroups(a, p) > most_workgroups(256))
+        return fail(CONV_ERR_UNSUPPORTED, "a sequence's grid beyond 2^24 - 1 workgroups");
     return CONV_OK;
 }
 

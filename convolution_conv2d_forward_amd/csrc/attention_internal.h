@@ -7,6 +7,10 @@
 
 namespace conv2d {
 
+// A launch counts its grid in work-items, in 32 bits: workgroups of `threads`
+// threads that it may have.  Calls of more take several launches.
+constexpr int64_t most_workgroups(int threads) { return 0xffffffffll / threads; }
+
 // ------------------------------------------------------------- linear ----
 
 struct LinearArgs {
@@ -86,6 +90,11 @@ struct AttnPlan {
     int32_t row_tiles, splits;
     int64_t ws_bytes;
 };
+
+// Workgroups of each sequence.
+inline int64_t sequence_workgroups(const AttnArgs& a, const AttnPlan& p) {
+    return (int64_t)a.heads_kv * p.row_tiles * p.splits;
+}
 
 hipError_t launch_attention_rows(int32_t dtype, const AttnArgs& a, hipStream_t s);
 AttnPlan plan_attention(int32_t dtype, const AttnArgs& a);

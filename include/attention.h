@@ -212,8 +212,10 @@ CONV2D_API conv_status_t attention_workspace_bytes(attention_desc_t d, int64_t b
  *                    where that is 0
  * Errors: INVALID_ARG for null or misaligned (16 bytes) pointers, negative
  * sizes, kv_len or q_len beyond 2^30 or a workspace that is too small;
- * UNSUPPORTED for grids beyond 2^31 workgroups; ALIAS if the bytes from
- * out's first to its last element overlap an input's or the workspace. */
+ * UNSUPPORTED for a sequence of 2^24 workgroups and more (some 2^31 rows, all
+ * heads together), and for more than 2^30 rows of a key head; ALIAS if the
+ * bytes from out's first to its last element overlap an input's or the
+ * workspace. */
 CONV2D_API conv_status_t attention_forward(attention_desc_t d, int64_t batch, int64_t q_len, int64_t kv_len,
                                            const void* q, const void* k, const void* v, const int32_t* q_lens,
                                            const int32_t* kv_lens, const int32_t* prefix_lens,

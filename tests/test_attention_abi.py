@@ -174,3 +174,20 @@ def test_reference_masks_by_hand():
     assert s(1, 4, 1, 3, window=2) == [[0, 1, 1, 0]]
     assert s(3, 3, 3, 3, docs=[0, 1, 3]) == [[1, 0, 0], [0, 1, 1], [0, 1, 1]]
     assert s(3, 3, 2, 2, causal=True) == [[1, 0, 0], [1, 1, 0], [0, 0, 0]]
+
+
+def test_attention_grids_beyond_a_launch():
+    """A launch holds 2^24 - 1 workgroups of 256 threads: many sequences may take
+    several, one sequence has to fit."""
+    m = cc()
+    s = (1 << 20, 1 << 10, 8)
+    d = m.attention_desc_create(m.make_attention_params(128, 128, 8, dtype="bf16", q_strides=s, k_strides=s, v_strides=s,
+                                                        out_strides=s))
+    assert m.attention_workspace_bytes(d, 1 << 20, 1, 1) == 0        # 2^27 workgroups
+    assert m.attention_workspace_bytes(d, 1, (1 << 24) - 128, 1) == 0   # 2^24 - 128 tiles of 128 rows
+    with pytest.raises(m.ConvError) as e:
+        m.attention_workspace_bytes(d, 1, 1 << 24, 1)
+    assert e.value.status == m.CONV_ERR_UNSUPPORTED
+    P = 1 << 40
+    assert m._lib.attention_forward(d.handle, 1, 1 << 24, 1, P, 2 * P, 3 * P, None, None, None, None, 0, None, 4 * P, None, 0,
+                                    None) == m.CONV_ERR_UNSUPPORTED
