@@ -218,7 +218,6 @@ hipError_t run_vec(const RopeArgs& a, hipStream_t s) {
     int64_t parts = (want + a.tokens - 1) / a.tokens;
     if (parts > steps) parts = steps;
     const int64_t waves = (int64_t)a.tokens * parts;
-    if (waves > 0x7fffffff) return hipErrorInvalidValue;
     qk_rope_vec<T, HALF, LPH><<<dim3((uint32_t)((waves + 3) / 4)), dim3(256), 0, s>>>(
         a, turns_of<4 * LPH>(a), (int)parts, make_divu32((uint32_t)parts), (uint32_t)waves);
     return hipGetLastError();
@@ -234,15 +233,37 @@ hipError_t run(bool vec, const RopeArgs& a, hipStream_t s) {
     }
     const int heads = a.heads_q + (a.v ? 2 : 1) * a.heads_kv;
     const int64_t waves = (int64_t)a.tokens * heads;
-    if (waves > 0xfffffff0ll) return hipErrorInvalidValue;
-    qk_rope_any<T, HALF><<<dim3((uint32_t)((waves + 3) / 4)), dim3(256), 0, s>>>(a, turns_of<ROPE_MAX_PAIRS>(a), make_divu32((uint32_t)heads),
-                                                                                 (uint32_t)waves);
+    qk_rope_any<T, HALF><<<dim3((uint32_t)((waves + 3) / 4)), dim3(256), 0, s>>>(
+        a, turns_of<ROPE_MAX_PAIRS>(a), make_divu32((uint32_t)heads), (uint32_t)waves);
     return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_qk_rope(int32_t dtype, int32_t layout, bool vec, const RopeArgs& a, hipStream_t s) {
+    // So many tokens take a wave each, or one for each of their heads.
+    const int heads = a.heads_q + (a.v ? 2 : 1) * a.heads_kv;
+    const int64_t most = most_workgroups(256) * 4 / (vec ? 1 : heads);
+    if (a.tokens > most) {
+        const int64_t es = dtype == CONV_DTYPE_F32 ? 4 : 2;
+        for (int64_t t = 0; t < a.tokens; t += most) {
+            RopeArgs c = a;
+            c.tokens = (int32_t)(a.tokens - t < most ? a.tokens - t : most);
+            c.qkv = (const char*)a.qkv + t * a.qkv_s * es;
+            c.q = (char*)a.q + t * a.q_s * es;
+            c.positions = a.positions + t;
+            if (a.slots) {
+                c.slots = a.slots + t;
+            } else {
+                c.k = (char*)a.k + t * a.k_s * es;
+                if (a.v) c.v = (char*)a.v + t * a.v_s * es;
+                c.cache_rows = a.cache_rows - t;
+            }
+            const hipError_t e = launch_qk_rope(dtype, layout, vec, c, s);
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
+    }
     const bool half = layout == ROPE_HALF;
     if (dtype == CONV_DTYPE_F32) return half ? run<float, true>(vec, a, s) : run<float, false>(vec, a, s);
     return half ? run<bf16, true>(vec, a, s) : run<bf16, false>(vec, a, s);

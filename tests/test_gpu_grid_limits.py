@@ -28,3 +28,30 @@ def test_attention_over_millions_of_short_sequences():
     out = torch.full_like(q, float("nan"))
     m.attention_forward(desc, q, k, v, out, kv_lens=lens, doc_offsets=docs)
     assert torch.equal(out, v * (lens * docs[:, 1]).to(bf16)[:, None, None, None])
+
+
+@pytest.mark.parametrize("d,tokens", [(2, 22_400_000), (8, (1 << 26) + 77)])
+@pytest.mark.parametrize("with_slots", [False, True])
+def test_rope_over_millions_of_tokens(with_slots, d, tokens):
+    """One query, key and value head, of 2 elements (a wave each) or 8 (a wave a
+    token); positions 0 and 1 by turns."""
+    m = cc()
+    qkv = torch.randn((tokens, 3 * d), device="cuda").to(bf16)
+    pos = (torch.arange(tokens, device="cuda") % 3 == 1).to(torch.int32)
+    slots = (tokens - 1 - torch.arange(tokens, device="cuda")).to(torch.int32) if with_slots else None
+    q, k, v = (torch.full((tokens, 1, d), float("nan"), dtype=bf16, device="cuda") for _ in "qkv")
+    desc = m.qk_rope_desc_create(m.make_qk_rope_params(1, 1, d, rotary_dim=2, dtype="bf16"))
+    m.qk_rope_forward(desc, qkv, None, None, pos, slots, q, k, v)
+    if with_slots:
+        k, v = k.flip(0), v.flip(0)
+    assert torch.equal(v[:, 0], qkv[:, 2 * d:])
+    for got, x in ((q, qkv[:, :d]), (k, qkv[:, d:2 * d])):
+        got = got[:, 0]
+        assert torch.equal(got[:, 2:], x[:, 2:])
+        still = pos == 0
+        assert torch.equal(got[still, :2], x[still, :2])
+        a, b = x[~still, 0].double(), x[~still, 1].double()
+        one = torch.ones((), dtype=torch.float64, device="cuda")
+        for have, want in ((got[~still, 0], a * one.cos() - b * one.sin()), (got[~still, 1], b * one.cos() + a * one.sin())):
+            # One rounding to bf16, and the products' and functions' errors.
+            assert ((have.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * (a.abs() + b.abs())).all()
