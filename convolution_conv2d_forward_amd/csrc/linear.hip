@@ -47,13 +47,25 @@ linear_tile_t pick(int32_t dtype, const LinearArgs& a) {
     if (!f32) offer(LINEAR_TILE_256, rounds(256, 1) * 1.9f);
     const RowsShape sh = rows_shape(f32, a);
     const int bytes = a.k * (f32 ? 4 : 2), rows = 16 * sh.mt, waves = sh.waves;
-    const float groups = (float)((a.m + rows - 1) / rows) * (float)((a.n + 15) / 16) / (float)cus;
+    const float groups = (float)(((int64_t)a.m + rows - 1) / rows) * (float)((a.n + 15) / 16) / (float)cus;
     const float alone = !a.vec ? 1.2f : sh.mt == 4 ? (f32 ? 0.6f : 0.33f) : sh.mt == 2 ? (f32 ? 0.55f : 0.25f) : 0.3f;
     const float unit = fmaxf(alone, groups * (float)sh.mt * (!a.vec ? 0.9f : f32 ? 0.35f : 0.15f));
     const float step = a.vec ? best : best * 1.5f;   // through registers
     if (5.0f + (float)((bytes + 128 * waves - 1) / (128 * waves)) * unit < 6.0f + (float)((bytes + 127) / 128) * step)
         return LINEAR_ROWS;
     return tile;
+}
+
+// Whether one launch holds the call's workgroups (linear_tile.h's persistent
+// ones: whether they count their tiles in 31 bits).
+bool one_launch(int32_t dtype, const LinearArgs& a, linear_tile_t tile) {
+    const auto blocks = [&](int64_t bm, int64_t bn) { return ((a.m + bm - 1) / bm) * ((a.n + bn - 1) / bn); };
+    if (tile == LINEAR_ROWS) {
+        const RowsShape sh = rows_shape(dtype == CONV_DTYPE_F32, a);
+        return blocks(16 * sh.mt, 16) <= most_workgroups(64 * sh.waves);
+    }
+    const int t = tile == LINEAR_TILE_64 ? 64 : 128;   // or more
+    return blocks(t, t) <= (a.vec ? 0x7fff0000 : most_workgroups(256));
 }
 
 }  // namespace
@@ -68,6 +80,18 @@ const char* linear_kernel_name(int32_t dtype, const LinearArgs& a) {
 
 hipError_t launch_linear(int32_t dtype, const LinearArgs& a, hipStream_t s) {
     const linear_tile_t tile = pick(dtype, a);
+    if (!one_launch(dtype, a, tile)) {
+        // Halves of the rows (a few rows of any width fit).
+        const int64_t es = dtype == CONV_DTYPE_F32 ? 4 : 2;
+        LinearArgs lo = a, hi = a;
+        lo.m = a.m / 2;
+        hi.m = a.m - lo.m;
+        hi.x = (const char*)a.x + lo.m * a.xs * es;
+        hi.y = (char*)a.y + lo.m * a.ys * es;
+        if (a.residual) hi.residual = (const char*)a.residual + lo.m * a.rs * es;
+        const hipError_t e = launch_linear(dtype, lo, s);
+        return e != hipSuccess ? e : launch_linear(dtype, hi, s);
+    }
     if (tile == LINEAR_ROWS) return launch_linear_rows(dtype, a, s);
     return dtype == CONV_DTYPE_F32 ? launch_linear_tile<float>(a, tile, s) : launch_linear_tile<bf16>(a, tile, s);
 }

@@ -168,10 +168,10 @@ struct RowsShape {
     int mt, waves;
 };
 inline RowsShape rows_shape(bool f32, const LinearArgs& a) {
-    const int64_t cus = device_cu_count(), n = (a.n + 15) / 16;
-    if (a.m <= 16 || (a.m + 15) / 16 * n <= cus * 3 / 4) return {1, 8};
+    const int64_t cus = device_cu_count(), m = a.m, n = (a.n + 15) / 16;
+    if (m <= 16 || (m + 15) / 16 * n <= cus * 3 / 4) return {1, 8};
     if (!a.vec) return {2, 8};
-    if ((a.m + 31) / 32 * n <= cus) return {2, f32 ? 8 : 4};
+    if ((m + 31) / 32 * n <= cus) return {2, f32 ? 8 : 4};
     return {a.m <= 32 ? 2 : 4, 4};
 }
 

@@ -187,7 +187,7 @@ __global__ __launch_bounds__(64 * NW) void linear_rows_ring(LinearArgs a, int bl
 
 template <int MT, int NT>
 dim3 grid_of(const LinearArgs& a, int& blocks_m) {
-    blocks_m = (a.m + 16 * MT - 1) / (16 * MT);
+    blocks_m = (int)(((int64_t)a.m + 16 * MT - 1) / (16 * MT));
     return dim3((uint32_t)((int64_t)blocks_m * ((a.n + 16 * NT - 1) / (16 * NT))));
 }
 

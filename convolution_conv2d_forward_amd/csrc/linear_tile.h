@@ -304,7 +304,6 @@ template <typename T, int W, int BM, int BN, int WM, int WN, int CPR, int S>
 hipError_t run(const LinearArgs& a, hipStream_t s) {
     typedef Tile<T, BM, BN, WM, WN, CPR, S> C;
     const int64_t tm = ((int64_t)a.m + BM - 1) / BM, tn = ((int64_t)a.n + BN - 1) / BN;
-    if (tm * tn > 0x7fff0000) return hipErrorInvalidValue;
     return with_act(a, [&](auto act) {
         if constexpr (W > 0) {
             const int64_t fit = (int64_t)device_cu_count() * (160 * 1024 / (C::LDS * 16)) & ~7;   // workgroups at once

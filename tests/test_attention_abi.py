@@ -191,3 +191,13 @@ def test_attention_grids_beyond_a_launch():
     P = 1 << 40
     assert m._lib.attention_forward(d.handle, 1, 1 << 24, 1, P, 2 * P, 3 * P, None, None, None, None, 0, None, 4 * P, None, 0,
                                     None) == m.CONV_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("rows", [(1 << 31) - 1, (1 << 31) - 15, (1 << 31) - 64])
+@pytest.mark.parametrize("k,n,dtype", [(1, 1, "bf16"), (8, 8, "bf16"), (4096, 16, "f32"), (8, 1 << 24, "f32")])
+def test_linear_rule_at_the_most_rows(k, n, dtype, rows):
+    """Roundings of the row count stay within their type: so many rows go to
+    tiles, or, where k is long, to workgroups of 64 rows."""
+    m = cc()
+    d = m.linear_desc_create(m.make_linear_params(k, n, dtype=dtype))
+    assert m.linear_desc_kernel_name(d, rows) == m.linear_desc_kernel_name(d, 1 << 28)

@@ -55,3 +55,17 @@ def test_rope_over_millions_of_tokens(with_slots, d, tokens):
         for have, want in ((got[~still, 0], a * one.cos() - b * one.sin()), (got[~still, 1], b * one.cos() + a * one.sin())):
             # One rounding to bf16, and the products' and functions' errors.
             assert ((have.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * (a.abs() + b.abs())).all()
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+def test_linear_over_a_billion_rows(shift):
+    """Rows of one element, at 2-byte boundaries, so through registers: a
+    workgroup for each 64."""
+    m, rows = cc(), (1 << 30) + 1000
+    x = torch.empty(rows + shift, dtype=bf16, device="cuda")
+    x.view(torch.int16).random_(128, 20000)   # normal numbers of all sizes
+    x = x[shift:, None]
+    y = torch.full((rows, 1), float("nan"), dtype=bf16, device="cuda")
+    desc = m.linear_desc_create(m.make_linear_params(1, 1, dtype="bf16"))
+    m.linear_forward(desc, x, torch.ones((1, 1), dtype=bf16, device="cuda"), None, None, y)
+    assert torch.equal(x, y)
