@@ -3,6 +3,7 @@
 // qk_rope_forward checks seven tensors; in Python that took 2.4 of the 7.2 us
 // that the call costs the host.
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 namespace {
@@ -16,7 +17,7 @@ int64_t entry(PyObject* tuple, Py_ssize_t i) {
 
 // tensor(t, what, dtype, shape, strides): strides None stands for a dense
 // tensor; dimensions of length 1 may have any stride.  t None gives None.
-PyObject* tensor(PyObject*, PyObject* const* args, Py_ssize_t n) {
+PyObject* check(PyObject* const* args, Py_ssize_t n) {
     if (n != 5 || !PyUnicode_Check(args[1]) || !THPDtype_Check(args[2]) || !PyTuple_Check(args[3]) ||
         !(args[4] == Py_None || PyTuple_Check(args[4]))) {
         PyErr_SetString(PyExc_TypeError, "tensor(t, what, dtype, shape, strides)");
@@ -31,6 +32,7 @@ PyObject* tensor(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (t.scalar_type() != reinterpret_cast<THPDtype*>(args[2])->scalar_type || !t.is_cuda())
         return PyErr_Format(PyExc_TypeError, "%s: a GPU tensor of %R expected, got one of %s on %s", what, args[2],
                             c10::toString(t.scalar_type()), t.device().str().c_str());
+    if (t.layout() != at::kStrided) return PyErr_Format(PyExc_TypeError, "%s: a strided tensor expected", what);
     const at::IntArrayRef sizes = t.sizes(), strides = t.strides();
     bool fits = (Py_ssize_t)sizes.size() == PyTuple_GET_SIZE(args[3]);
     for (size_t i = 0; fits && i < sizes.size(); ++i) fits = sizes[i] == entry(args[3], (Py_ssize_t)i);
@@ -53,7 +55,24 @@ PyObject* tensor(PyObject*, PyObject* const* args, Py_ssize_t n) {
             return nullptr;
         }
     }
-    return PyLong_FromVoidPtr(t.data_ptr());
+    void* p = t.data_ptr();
+    if (!p && t.numel() > 0) return PyErr_Format(PyExc_TypeError, "%s: a tensor without memory", what);
+    return PyLong_FromVoidPtr(p);
+}
+
+// torch throws where a tensor has no plain sizes, strides or memory (symbolic
+// sizes, a tensor under vmap); from a C entry that would end the process.
+PyObject* tensor(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    try {
+        return check(args, n);
+    } catch (python_error& e) {
+        e.restore();
+        return nullptr;
+    } catch (const c10::Error& e) {
+        return PyErr_Format(PyExc_TypeError, "%S: %s", args[1], e.what_without_backtrace());
+    } catch (const std::exception& e) {
+        return PyErr_Format(PyExc_RuntimeError, "%S: %s", args[1], e.what());
+    }
 }
 
 PyMethodDef methods[] = {{"tensor", (PyCFunction)(void (*)())tensor, METH_FASTCALL,
