@@ -84,10 +84,10 @@ class _Desc:
     """Owns a descriptor of include/attention.h; destroyed with the object."""
 
     def __init__(self, kind, params):
-        h = ctypes.c_void_p()
-        _check(getattr(_lib, kind + "_desc_create")(ctypes.byref(params), ctypes.byref(h)))
         if _tensor is None:
             _load()
+        h = ctypes.c_void_p()
+        _check(getattr(_lib, kind + "_desc_create")(ctypes.byref(params), ctypes.byref(h)))
         self.kind, self.handle = kind, h
         self.params = type(params)()
         ctypes.memmove(ctypes.byref(self.params), ctypes.byref(params), ctypes.sizeof(params))
@@ -124,7 +124,10 @@ def _load():
     global _tensor, _f32, _bf16, _i32
     import torch
 
-    from ._marshal import tensor
+    try:
+        from ._marshal import tensor
+    except ImportError as e:
+        raise ImportError(f"the binding's tensor checks (_marshal.so) are not built, build.py makes them: {e}") from e
     _tensor, _f32, _bf16, _i32 = tensor, torch.float32, torch.bfloat16, torch.int32
 
 

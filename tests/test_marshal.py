@@ -51,3 +51,15 @@ refused(x, TypeError)
 def test_tensors_without_plain_memory_are_refused(case):
     r = subprocess.run([sys.executable, "-c", SETUP + case], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_missing_checks_are_named_before_a_descriptor_is_made(monkeypatch):
+    import convolution_conv2d_forward_amd as cc
+    from convolution_conv2d_forward_amd import attention
+    made = []
+    monkeypatch.setattr(attention, "_tensor", None)
+    monkeypatch.setitem(sys.modules, "convolution_conv2d_forward_amd._marshal", None)
+    monkeypatch.setattr(attention._lib, "linear_desc_create", lambda *a: made.append(a) or 0)
+    with pytest.raises(ImportError, match="_marshal.so"):
+        cc.linear_desc_create(cc.make_linear_params(8, 8))
+    assert not made, "a handle that nothing would destroy"
