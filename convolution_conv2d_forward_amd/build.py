@@ -22,7 +22,8 @@ SOURCES = ["conv2d_api.cpp", "igemm_f32.hip", "igemm_bf16.hip", "depthwise.hip",
            "direct.hip", "fused_pw_dw.hip", "fused_dw_pw.hip", "grouped.hip", "qdepthwise.hip",
            "qfused_dw_pw.hip", "qfused_pw_dw.hip", "igemm_i8.hip", "probe_copy.hip", "winograd_f32.hip",
            "winograd4_f32.hip", "pointwise_f32.hip", "pw_gemm_f32.hip", "pw_narrow_f32.hip", "small_f32.hip",
-           "attention_api.cpp", "linear.hip", "linear_rows.hip", "linear_f32.hip", "linear_bf16.hip", "qk_rope.hip", "attention_any.hip", "attention_f32.hip", "attention_bf16.hip", "attention_rows.hip"]
+           "attention_api.cpp", "linear.hip", "linear_rows.hip", "linear_f32.hip", "linear_bf16.hip", "qk_rope.hip",
+           "attention_any.hip", "attention_f32.hip", "attention_bf16.hip", "attention_rows.hip"]
 
 FLAGS = ["-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC", "-fvisibility=hidden", "-Wall", "-Wno-unused-function",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -45,13 +46,18 @@ def _compile(src, verbose):
 
 
 def _build_marshal(verbose):
-    """The binding's tensor checks, against the headers of the installed torch (host code only)."""
+    """The binding's tensor checks, against the headers of the installed torch (host code only).  The C library needs
+    neither, so without torch they are left out, with a note: the Python binding, which uses torch, says so too."""
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except ImportError as e:
+        print(f"_marshal.so is not built: {e}", flush=True)
+        return
     root = os.path.dirname(os.path.abspath(torch.__file__))
     tmp = MARSHAL + ".tmp"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
+    cmd = [HIPCC, "-x", "c++", "-no-hip-rt", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *("-I" + os.path.join(root, d) for d in ("include", "include/torch/csrc/api/include")),
            "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.cpp"), "-o", tmp,
@@ -60,7 +66,7 @@ def _build_marshal(verbose):
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stdout}{r.stderr}")
+        raise RuntimeError(f"hipcc failed on marshal.cpp:\n{r.stdout}{r.stderr}")
     os.replace(tmp, MARSHAL)
 
 

@@ -63,3 +63,26 @@ def test_missing_checks_are_named_before_a_descriptor_is_made(monkeypatch):
     with pytest.raises(ImportError, match="_marshal.so"):
         cc.linear_desc_create(cc.make_linear_params(8, 8))
     assert not made, "a handle that nothing would destroy"
+
+
+def _build_script(monkeypatch, path):
+    import importlib.util
+    spec = importlib.util.spec_from_file_location("_build", os.path.join(ROOT, "convolution_conv2d_forward_amd", "build.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    monkeypatch.setattr(m, "MARSHAL", str(path))
+    return m
+
+
+def test_library_builds_without_torch(monkeypatch, tmp_path, capsys):
+    m = _build_script(monkeypatch, tmp_path / "_marshal.so")
+    monkeypatch.setitem(sys.modules, "torch", None)
+    m._build_marshal(False)
+    assert "_marshal.so is not built" in capsys.readouterr().out and not os.listdir(tmp_path)
+
+
+def test_checks_build_with_the_librarys_own_compiler(monkeypatch, tmp_path):
+    m = _build_script(monkeypatch, tmp_path / "_marshal.so")
+    monkeypatch.setenv("CXX", "/nonexistent/compiler")
+    m._build_marshal(False)
+    assert os.listdir(tmp_path) == ["_marshal.so"]
