@@ -136,12 +136,13 @@ __device__ __forceinline__ u32x4 load_chunk(const T* p, int left) {
 }
 
 // The same for bf16 put together from the five words that a chunk between
-// 4-byte boundaries touches.  Where few waves wait for few chunks that is
-// faster than a load of 16 bytes at such an address (24x4097x1126: 22.7 us
-// against 36.0), where many are loaded slower (4001x1003x4003: 138 against 112).
-__device__ __forceinline__ u32x4 load_words(const bf16* p, int left) {
+// 4-byte boundaries touches, which hold an element before p and one past p + 7:
+// not for chunks at a row's `end`.  Where few waves wait for few chunks that is
+// faster than a load of 16 bytes at such an address (24x4097x1126: 17.1 us
+// against 27.0), where many are loaded slower (4001x1003x4003: 138 against 112).
+__device__ __forceinline__ u32x4 load_words(const bf16* p, bool end, int left) {
     typedef u32x4 __attribute__((aligned(4))) words;
-    if (left < 8) return load_chunk<bf16>(p, left);
+    if (end) return load_chunk<bf16>(p, left);
     const uint32_t odd = (uint32_t)(uintptr_t)p & 2;
     const uint32_t* q = (const uint32_t*)((uintptr_t)p - odd);
     const u32x4 d = *(const words*)q;
@@ -153,7 +154,7 @@ __device__ __forceinline__ u32x4 load_words(const bf16* p, int left) {
     r[3] = __builtin_amdgcn_alignbit(d4, d[3], odd * 8);
     return r;
 }
-__device__ __forceinline__ u32x4 load_words(const float* p, int left) { return load_chunk<float>(p, left); }
+__device__ __forceinline__ u32x4 load_words(const float* p, bool, int left) { return load_chunk<float>(p, left); }
 
 // Kernels of a call: few rows of x, or few tiles of a long k (linear_rows.hip),
 // or tiles of as many rows of x and w (linear_tile.h), 128 with two workgroups

@@ -62,7 +62,7 @@ template <typename T, int MT, int NT, int NW, int U>
 __global__ __launch_bounds__(64 * NW) void linear_rows(LinearArgs a, int blocks_m) {
     constexpr int C = Vec<T>::chunk, UNIT = 8 * C;
     __shared__ __align__(16) f32x4 red[NW * NT * MT * 64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int m0 = blockIdx.x % blocks_m * 16 * MT, n0 = blockIdx.x / blocks_m * 16 * NT, r = lane & 15, g = lane >> 4;
     // Rows past the end repeat the last one; their results are not stored.
     const T *w[NT], *x[MT];
@@ -78,10 +78,12 @@ __global__ __launch_bounds__(64 * NW) void linear_rows(LinearArgs a, int blocks_
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int k = k0 + u * NW * UNIT + h * 4 * C, left = a.k - k - g * C;   // elements from this lane's first
+                // Of the wave's chunks of this step, one starts or ends its row, or lies past it.
+                const bool end = k == 0 || k + 4 * C >= a.k;
 #pragma unroll
-                for (int i = 0; i < NT; ++i) fw[u][h][i] = load_words(w[i] + k, left);
+                for (int i = 0; i < NT; ++i) fw[u][h][i] = load_words(w[i] + k, end, left);
 #pragma unroll
-                for (int j = 0; j < MT; ++j) fx[u][h][j] = load_words(x[j] + k, left);
+                for (int j = 0; j < MT; ++j) fx[u][h][j] = load_words(x[j] + k, end, left);
             }
 #pragma unroll
         for (int u = 0; u < U; ++u)
