@@ -1,9 +1,11 @@
 // C ABI of include/attention.h: descriptors, argument checks, dispatch.  Host
 // code only.
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <cstring>
 #include <new>
+#include <utility>
 
 #include "attention_internal.h"
 
@@ -160,6 +162,20 @@ conv_status_t check_attn_grid(const AttnArgs& a, const AttnPlan& p) {
 View span_view(const void* ptr, const int64_t* s, int64_t batch, int64_t len, int64_t heads, int64_t d, int64_t es) {
     if (!ptr || batch == 0 || len == 0) return View{(uintptr_t)ptr, 0, 0, 0};
     return View{(uintptr_t)ptr, 1, 0, ((batch - 1) * s[0] + (len - 1) * s[1] + (heads - 1) * s[2] + d) * es};
+}
+
+// Whether a tensor's dimensions lie within each other, so that no two elements
+// share memory: each stride reaches past all that the smaller ones span.
+bool nested(const int64_t* s, int64_t batch, int64_t len, int64_t heads, int64_t d) {
+    std::pair<int64_t, int64_t> dims[3] = {{s[0], batch}, {s[1], len}, {s[2], heads}};
+    std::sort(dims, dims + 3);
+    int64_t span = d;
+    for (const auto& [stride, n] : dims) {
+        if (n <= 1) continue;
+        if (stride < span) return false;
+        span += (n - 1) * stride;
+    }
+    return true;
 }
 
 }  // namespace
@@ -441,6 +457,8 @@ conv_status_t attention_forward(attention_desc_t d, int64_t batch, int64_t q_len
                         flat_view(prefix_lens, 4 * batch),
                         flat_view(doc_offsets, 4 * batch * ((int64_t)n_docs + 1)),
                         flat_view(p.has_slopes ? slopes : nullptr, 4 * (int64_t)p.heads_q)};
+    if (!nested(p.out_strides, batch, q_len, p.heads_q, p.head_dim))
+        return fail(CONV_ERR_ALIAS, "rows of out share memory");
     if (views_overlap(ov, wv)) return fail(CONV_ERR_ALIAS, "out overlaps the workspace");
     for (const View& iv : in)
         if (views_overlap(ov, iv) || views_overlap(wv, iv))

@@ -158,7 +158,8 @@ typedef struct {
     /* Strides of (batch, token, head) of each tensor; a head's head_dim
      * elements are contiguous.  Every stride is a multiple of 16 bytes, at
      * least 0 for the inputs (0 repeats one batch, token or head) and at
-     * least head_dim for the output. */
+     * least head_dim for the output, each of whose strides reaches past what
+     * the smaller ones span (any order of dimensions, any gaps). */
     int64_t q_strides[3], k_strides[3], v_strides[3], out_strides[3];
     int32_t heads_q, heads_kv;  /* heads_kv divides heads_q; query head h reads key head h / (heads_q / heads_kv) */
     int32_t head_dim;           /* <= 256, a multiple of 16 bytes */
@@ -213,9 +214,9 @@ CONV2D_API conv_status_t attention_workspace_bytes(attention_desc_t d, int64_t b
  * Errors: INVALID_ARG for null or misaligned (16 bytes) pointers, negative
  * sizes, kv_len or q_len beyond 2^30 or a workspace that is too small;
  * UNSUPPORTED for a sequence of 2^24 workgroups and more (some 2^31 rows, all
- * heads together), and for more than 2^30 rows of a key head; ALIAS if the
- * bytes from out's first to its last element overlap an input's or the
- * workspace. */
+ * heads together), and for more than 2^30 rows of a key head; ALIAS if rows of
+ * out share memory, or if the bytes from out's first to its last element
+ * overlap an input's or the workspace. */
 CONV2D_API conv_status_t attention_forward(attention_desc_t d, int64_t batch, int64_t q_len, int64_t kv_len,
                                            const void* q, const void* k, const void* v, const int32_t* q_lens,
                                            const int32_t* kv_lens, const int32_t* prefix_lens,

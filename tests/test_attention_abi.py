@@ -201,3 +201,22 @@ def test_linear_rule_at_the_most_rows(k, n, dtype, rows):
     m = cc()
     d = m.linear_desc_create(m.make_linear_params(k, n, dtype=dtype))
     assert m.linear_desc_kernel_name(d, rows) == m.linear_desc_kernel_name(d, 1 << 28)
+
+
+@pytest.mark.parametrize("strides,status", [
+    ((6400, 64, 64), "ALIAS"), ((64, 256, 64), "ALIAS"), ((640, 256, 64), "ALIAS"), ((6400, 128, 64), "ALIAS"),
+    ((6400, 64, 128), "ALIAS"),                                   # a token's heads 0 and 1 are 2 tokens apart
+    ((1280, 256, 64), "OK"), ((256, 512, 64), "OK"), ((1280, 64, 320), "OK"), ((1600, 320, 80), "OK"),
+], ids=str)
+def test_attention_rows_of_out_share_no_memory(strides, status):
+    """2 sequences, 5 tokens, 4 heads of 64.  Accepted ones go on to the check of
+    the workspace, which follows."""
+    m = cc()
+    d = m.attention_desc_create(m.make_attention_params(4, 4, 64, **_strides(out_strides=strides)))
+    P = 1 << 30
+    status_of = lambda ws: m._lib.attention_forward(  # noqa: E731
+        d.handle, 2, 5, 5000, P, 2 * P, 3 * P, None, None, None, None, 0, None, 4 * P, ws, 1 << 30, None)
+    need = m.attention_workspace_bytes(d, 2, 5, 5000)
+    assert need > 0
+    assert status_of(4 * P) == m.CONV_ERR_ALIAS
+    assert ("share" in m.conv2d_last_error()) == (status == "ALIAS"), m.conv2d_last_error()
