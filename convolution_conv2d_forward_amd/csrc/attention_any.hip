@@ -167,7 +167,7 @@ __global__ __launch_bounds__(256) void attention_any(AttnArgs a) {
 #pragma unroll
         for (int d = 0; d < DP / 16; ++d) o[d] *= fade;
         if constexpr (sizeof(T) == 2) {
-            bf16x8 fp;
+            bf16x8 fp;   // rounded, as in attention_tile
 #pragma unroll
             for (int i = 0; i < 8; ++i) fp[i] = (bf16)s[i >> 2][i & 3];
 #pragma unroll

@@ -194,9 +194,16 @@ __global__ __launch_bounds__((64 * RowsAttn<T, DP>::NW), (RowsAttn<T, DP>::OCC))
 #pragma unroll
         for (int d = 0; d < OUT; ++d) o[d] *= fade;
         if constexpr (sizeof(T) == 2) {
-            bf16x8 fp;
+            // The weights as a bf16 number and what it leaves, so 16 bits of
+            // them: the products wait for memory, not the matrix cores for
+            // them (16x4096 keys of 8 heads of 128: 62.6 us, 62.0 without;
+            // 28x30 of 12 heads of 256: 19.4 and 18.8).
+            bf16x8 fp, fl;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) fp[i] = (bf16)p[i >> 2][i & 3];
+            for (int i = 0; i < 8; ++i) {
+                fp[i] = (bf16)p[i >> 2][i & 3];
+                fl[i] = (bf16)(p[i >> 2][i & 3] - (float)fp[i]);
+            }
 #pragma unroll
             for (int c = 0; c < VC; ++c)
 #pragma unroll
@@ -207,6 +214,8 @@ __global__ __launch_bounds__((64 * RowsAttn<T, DP>::NW), (RowsAttn<T, DP>::OCC))
                         w[j] = __builtin_amdgcn_perm(f.v[2 * j + 1][c][e >> 1], f.v[2 * j][c][e >> 1],
                                                      e & 1 ? 0x07060302u : 0x05040100u);
                     o[c * 8 + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), fp,
+                                                                              o[c * 8 + e], 0, 0, 0);
+                    o[c * 8 + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), fl,
                                                                               o[c * 8 + e], 0, 0, 0);
                 }
         } else {

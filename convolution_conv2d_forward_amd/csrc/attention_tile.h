@@ -322,7 +322,12 @@ __global__ __launch_bounds__(256, (TileAttn<T, DP, KW>::OCC)) void attention_til
         }
         const float base = a0 - (m_run == -INFINITY ? 0.0f : m_run);   // nothing seen yet: every weight is 0
         // The weights: bf16 ones are rounded before the product, as the values
-        // are; their sum is of the unrounded ones.
+        // are; their sum is of the unrounded ones.  Adding the product with what
+        // the rounding leaves, as attention_rows does, takes the difference
+        // from unrounded weights from 2.4e-3 (rms, of the outputs' rms) to 1e-4,
+        // and from 64 bits, after the outputs' own rounding, from 2.2e-3 to
+        // 1.7e-3, but 8192 causal capped rows of 16 heads of 128 over 4 from 354
+        // to 450 us, uncapped ones from 289 to 395.
         bf16x8 p[2 * TK];
 #pragma unroll
         for (int t = 0; t < 2 * TK; ++t)

@@ -20,11 +20,12 @@
  *
  * Element types are CONV_DTYPE_F32 and CONV_DTYPE_BF16 (I8 returns
  * UNSUPPORTED).  Sums, norms, angles and softmax statistics are held in fp32
- * or more for both; a bf16 result is rounded once, to nearest even (in
- * attention_forward the softmax weights are rounded to bf16 before they meet
- * bf16 values on the matrix cores, and a capped score may be off by softcap *
- * 2^-21 up to a softcap of 512, by 2^-21 of itself beyond).  Strides count
- * elements.
+ * or more for both; a bf16 result is rounded once, to nearest even.  In
+ * attention_forward a bf16 call's softmax weights meet the values on the matrix
+ * cores with 16 bits where at most 16 rows share a key head (q_len heads_q /
+ * heads_kv: single tokens), rounded to bf16 beyond, and a capped score may be
+ * off by softcap * 2^-21 up to a softcap of 512, by 2^-21 of itself beyond.
+ * Strides count elements.
  */
 #ifndef ATTENTION_MI355X_H
 #define ATTENTION_MI355X_H

@@ -84,3 +84,18 @@ def test_small_caps(cap, with_slopes, q_len, dtype):
     got = _call(q.cuda(), k.cuda(), v.cuda(), c, slopes=slopes)
     want, tol = attention64(q, k, v, c, slopes=slopes)
     assert_within(got, want, tol, f"cap {cap}")
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=30.0, causal=True), dict(window=100, causal=True)],
+                         ids=lambda kw: "-".join(kw) or "plain")
+@pytest.mark.parametrize("b,q_len,kv_len,hq,hk,d", [(3, 1, 700, 8, 2, 128), (2, 4, 300, 4, 2, 64), (1, 2, 5000, 16, 2, 256),
+                                                    (4, 1, 33, 6, 6, 96)])
+def test_few_rows_keep_16_bits_of_the_weights(b, q_len, kv_len, hq, hk, d, kw):
+    """bf16: the bound of fp32 weights, 2^-16 of the values' weighted size for the
+    weights' two parts (each off by 2^-8 of what it stands for), and the output's
+    rounding."""
+    q, k, v = _inputs(b, q_len, kv_len, hq, hk, d, "bf16", 9)
+    got = _call(q.cuda(), k.cuda(), v.cuda(), {"dtype": "bf16", **kw})
+    want, tol = attention64(q, k, v, {"dtype": "f32", **kw})
+    size, _ = attention64(q, k, v.abs(), {"dtype": "f32", **kw})
+    assert_within(got, want, tol + 2.0 ** -16 * size + ROUND["bf16"] * want.abs())
