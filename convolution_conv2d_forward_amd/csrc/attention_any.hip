@@ -385,14 +385,15 @@ AttnPlan plan_attention(int32_t dtype, const AttnArgs& a) {
     AttnPlan p{};
     // A tile's keys within 32-bit byte offsets.
     const bool near = a.k_s[1] < 1 << 24 && a.v_s[1] < 1 << 24;
-    // 17 to 32 rows in bf16, 32 rows of 128 over 8x4096 keys: 39.5 us in one
-    // tile, 48.6 in two of 16 rows.
+    // 17 to 32 rows in bf16, 32 rows of 128 over 8x4096 keys: 36.8 us in one
+    // tile, 47.8 in two of 16 rows.
     p.kernel = a.rows <= (dtype == CONV_DTYPE_F32 ? 32 : 16)       ? ATTN_ROWS
                : near ? ATTN_TILE_128
                       : ATTN_ANY;
     // Heads beyond 128 leave room for one workgroup on a CU in either size:
     // 2500 causal rows of 16 heads of 256 over 4 (316 tiles of 128) take 130 us
-    // in them and 147 in tiles of 64, 1300 rows (164 tiles) 57.4 and 52.5.
+    // in them and 149 in tiles of 64, 1300 rows (164 tiles) 69 and 53 with the
+    // keys undivided.
     const int64_t cus = device_cu_count();
     if (p.kernel == ATTN_TILE_128 && !(dtype == CONV_DTYPE_F32 && a.d > 128) &&
         (int64_t)a.batch * a.heads_kv * ((a.rows + 127) / 128) < (a.d > 128 ? cus * 3 / 4 : cus * 2))
@@ -401,12 +402,14 @@ AttnPlan plan_attention(int32_t dtype, const AttnArgs& a) {
     p.row_tiles = (a.rows + tile - 1) / tile;
     // Few row tiles leave compute units without work: the keys are then split.
     const int64_t tiles = (int64_t)a.batch * a.heads_kv * p.row_tiles;
-    // Workgroups wanted, and keys for each at least.  Two a unit even out rows
-    // of different lengths (5322 causal rows of 4 heads of 64: 77.6 us with
-    // one, 51.7 with two).  The partial results of many rows cost as much as a
-    // few hundred keys: 1000 causal rows of 16 heads of 128 over 4 take 22.8 us
-    // undivided, 27.5 in two; 538 of 12 fp32 heads of 128 48.6 us in parts of
-    // 256 keys, 39.2 of 512.
+    // Workgroups wanted, and keys for each part but the last.  Two a unit even
+    // out rows of different lengths (5322 causal rows of 4 heads of 64: 63.4 us
+    // undivided, 43.1 in two).  The partial results of many rows cost as much as
+    // a few hundred keys: 1000 causal rows of 16 heads of 128 over 4 take 22.2 us
+    // undivided, 26.9 in two; 538 of 12 fp32 heads of 128 50.1 us undivided,
+    // 37.7 in two, 36.0 in three.  Keys just above a part's are divided all the
+    // same, which wide bf16 heads pay for: 1300 rows of 256 73 us in two, 53
+    // undivided, but 1700 72 and 92.
     const bool f32 = dtype == CONV_DTYPE_F32;
     int64_t want = 2 * cus;
     int64_t keys = f32 ? 512 : tiles * 2 >= cus ? 1024 : 256;
@@ -418,7 +421,8 @@ AttnPlan plan_attention(int32_t dtype, const AttnArgs& a) {
         keys = tiles >= cus ? 1024 : tiles * 2 >= cus ? 512 : 128;
     }
     // Of wide fp32 rows one workgroup fits on a unit: the nearest, not the next
-    // number of parts (252 tiles of 128: 108 us in two, 116 in three).
+    // number of parts (4096 causal rows of 4 heads of 128, 256 tiles: 194 us in
+    // two, 203 in three).
     int64_t s = tiles < want ? (want + (f32 && p.kernel != ATTN_ROWS ? tiles / 2 : tiles - 1)) / tiles : 1;
     const int64_t most = ((int64_t)a.kv_len + keys - 1) / keys;
     if (s > most) s = most;

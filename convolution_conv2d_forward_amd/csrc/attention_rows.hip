@@ -28,12 +28,12 @@ struct RowsAttn {
     static constexpr int KS = DP * (int)sizeof(T) / 64;               // 64-byte product steps over a row
     static constexpr int VC = (DP / C + 15) / 16;                     // 16-chunk groups of a row of V
     // Keys of a tile: rows of 1024 bytes spilled at 32 (8x4096 keys of 8 heads of
-    // 256 fp32: 157 us, 130 at 16; a few keys: 18.4 and 12.5).
+    // 256 fp32: 157 us, 128 at 16; one token over 25 keys: 18.4 and 12.5).
     static constexpr int BK = DP * (int)sizeof(T) > 512 ? 16 : 32, NT = BK / 16, NJ = BK / 4;
     static constexpr int OUT = VC * C;                                // 16x16 output blocks
     // A tile takes a quarter of the row's bytes in registers: rows to 256 bytes
     // leave room for two waves on a SIMD, each with two tiles.  Two tiles of
-    // 256 bf16 leave no register (16x4096 keys: 115 us, 109 with one); of 128
+    // 256 bf16 leave no register (16x4096 keys: 128 us, 110 with one); of 128
     // fp32, without the permutes, they pay (115, 122 with one).
     static constexpr int RB = DP * (int)sizeof(T), NBUF = DP <= 128 ? 2 : 1, OCC = RB <= 256 ? 2 : 1, NW = 4;
     u32x4 k[NT][KS];

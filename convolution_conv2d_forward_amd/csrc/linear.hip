@@ -16,16 +16,16 @@ namespace {
 //                                            fp32 0.3 / 0.55 / 0.6
 //   for each workgroup a CU has, 64 rows     0.6 and 1.4
 // and through registers 1.2, or 1.8 for each with 32 rows.  It takes up to 32
-// rows always, and few tiles of a long k (64x4096x4096 bf16: 14.8 us against
-// 23.2 in tiles; 64x4096x11264: 35.3 against 28.0).
+// rows always, and few tiles of a long k (64x4096x4096 bf16: 15.0 us against
+// 23.0 in tiles; 64x4096x11264: 35.3 against 28.3).
 //
 // Tiles take rounds of workgroups, and in each for a step of 128 bytes (us,
 // with all CUs at work), after some 6 us:
 //              256    128 by pairs    128 deep    64
 //   bf16       1.9    1.2             0.72        0.49, one a CU 0.30
 //   fp32       -      3.85            2.07        1.1, one a CU 0.65
-// (2048x4096x4096 bf16: 111 us in tiles of 256, 80 in pairs of 128, 93 in
-// deep ones, 129 in tiles of 64.)
+// (2048x4096x4096 bf16: 109 us in tiles of 256, 78 in pairs of 128, 83 in
+// deep ones, 125 in tiles of 64.)
 linear_tile_t pick(int32_t dtype, const LinearArgs& a) {
     if (a.m <= 32) return LINEAR_ROWS;
     const bool f32 = dtype == CONV_DTYPE_F32;

@@ -139,7 +139,7 @@ __device__ __forceinline__ u32x4 load_chunk(const T* p, int left) {
 // 4-byte boundaries touches, which hold an element before p and one past p + 7:
 // not for chunks at a row's `end`.  Where few waves wait for few chunks that is
 // faster than a load of 16 bytes at such an address (24x4097x1126: 17.1 us
-// against 27.0), where many are loaded slower (4001x1003x4003: 138 against 112).
+// against 27.0), where many are loaded slower (4001x1003x4003: 132 against 71).
 __device__ __forceinline__ u32x4 load_words(const bf16* p, bool end, int left) {
     typedef u32x4 __attribute__((aligned(4))) words;
     if (end) return load_chunk<bf16>(p, left);
