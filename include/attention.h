@@ -210,7 +210,8 @@ CONV2D_API conv_status_t attention_workspace_bytes(attention_desc_t d, int64_t b
  * Its score is s = scale * q.k, capped, minus slopes[h] * |p - j|.  Rows that
  * see no key, and rows from Q on, are zero.  Elements of k and v that a row
  * does not see do not reach it, whatever they hold; keys from K on are not
- * read at all.
+ * read at all.  An infinity that it sees makes that element of the row infinite
+ * (NaN, as 0 * inf, where its weight is below fp32's range).
  *   workspace        at least attention_workspace_bytes, 16-byte aligned,
  *                    scratch of this call alone until it ends; may be null
  *                    where that is 0

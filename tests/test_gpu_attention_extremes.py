@@ -99,3 +99,24 @@ def test_few_rows_keep_16_bits_of_the_weights(b, q_len, kv_len, hq, hk, d, kw):
     want, tol = attention64(q, k, v, {"dtype": "f32", **kw})
     size, _ = attention64(q, k, v.abs(), {"dtype": "f32", **kw})
     assert_within(got, want, tol + 2.0 ** -16 * size + ROUND["bf16"] * want.abs())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("b,q_len,kv_len,hq,hk,d", [(3, 1, 700, 8, 2, 128), (2, 4, 300, 4, 2, 64), (1, 2, 900, 16, 2, 256),
+                                                    (4, 1, 33, 6, 6, 96), (1, 70, 200, 4, 2, 64)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_infinities_that_all_rows_see(causal, b, q_len, kv_len, hq, hk, d, dtype):
+    """Also where weights have few bits or are powers of two: an infinity stays
+    one, and its sign; both signs, or NaN, make NaN."""
+    q, k, v = _inputs(b, q_len, kv_len, hq, hk, d, dtype, 10)
+    q[0, 0] = 0                       # equal scores: weights of one
+    last = kv_len - q_len             # seen by all rows, causal or not
+    v[0, last // 2, 0, 1] = math.inf
+    v[:, last, hk - 1, 2] = -math.inf
+    v[0, 0, 0, 3], v[0, last // 3, 0, 3] = math.inf, -math.inf
+    v[0, 1 % (last + 1), hk - 1, d - 1] = math.nan
+    c = {"dtype": dtype, "causal": causal}
+    got = _call(q.cuda(), k.cuda(), v.cuda(), c)
+    want, tol = attention64(q, k, v, c)
+    assert torch.isinf(want).any() and torch.isnan(want).any()
+    assert_within(got, want, tol)
