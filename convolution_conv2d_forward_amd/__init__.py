@@ -18,8 +18,10 @@ Names and argument order follow the C ABI:
     conv2d_last_error
 plus ``make_params`` (keyword construction of a params struct).  The operators
 of an attention layer (include/attention.h: linear_forward, qk_rope_forward,
-attention_forward and their descriptors) are bound in attention.py and exported
-here too.
+attention_forward and their descriptors) are bound in attention.py, those of a
+decoder layer over a paged cache (include/decoder.h: kv_cache_store,
+kv_cache_load, paged_attention_forward, block_norm_forward) in decoder.py; both
+are exported here too.
 """
 import ctypes
 import math
@@ -438,5 +440,11 @@ from .attention import (  # noqa: E402
     attention_workspace_bytes, linear_desc_create, linear_desc_destroy, linear_desc_kernel_name, linear_forward,
     linear_params_init, linear_params_t, make_attention_params, make_linear_params, make_qk_rope_params,
     qk_rope_desc_create, qk_rope_desc_destroy, qk_rope_forward, qk_rope_params_init, qk_rope_params_t)
+from .decoder import (  # noqa: E402
+    block_norm_desc_create, block_norm_desc_destroy, block_norm_forward, block_norm_params_init, block_norm_params_t,
+    kv_cache_desc_create, kv_cache_desc_destroy, kv_cache_load, kv_cache_params_init, kv_cache_params_t,
+    kv_cache_store, make_block_norm_params, make_kv_cache_params, make_paged_attention_params,
+    paged_attention_desc_create, paged_attention_desc_destroy, paged_attention_forward, paged_attention_params_init,
+    paged_attention_params_t, paged_attention_workspace_bytes)
 
 __all__ = [n for n in dir() if not n.startswith("_") and n not in ("ctypes", "math", "os")]

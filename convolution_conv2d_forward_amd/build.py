@@ -23,7 +23,8 @@ SOURCES = ["conv2d_api.cpp", "igemm_f32.hip", "igemm_bf16.hip", "depthwise.hip",
            "qfused_dw_pw.hip", "qfused_pw_dw.hip", "igemm_i8.hip", "probe_copy.hip", "winograd_f32.hip",
            "winograd4_f32.hip", "pointwise_f32.hip", "pw_gemm_f32.hip", "pw_narrow_f32.hip", "small_f32.hip",
            "attention_api.cpp", "linear.hip", "linear_rows.hip", "linear_f32.hip", "linear_bf16.hip", "qk_rope.hip",
-           "attention_any.hip", "attention_f32.hip", "attention_bf16.hip", "attention_rows.hip"]
+           "attention_any.hip", "attention_f32.hip", "attention_bf16.hip", "attention_rows.hip", "decoder_api.cpp",
+           "kv_cache.hip", "paged_attention.hip", "block_norm.hip"]
 
 FLAGS = ["-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC", "-fvisibility=hidden", "-Wall", "-Wno-unused-function",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

@@ -1,7 +1,7 @@
-// Checks of torch tensors for the binding of include/attention.h: the device
-// pointer of a tensor of the expected type, shape and strides.  A call of
-// qk_rope_forward checks seven tensors; in Python that took 2.4 of the 7.2 us
-// that the call costs the host.
+// Checks of torch tensors for the bindings of include/attention.h and
+// include/decoder.h: the device pointer of a tensor of the expected type, shape
+// and strides.  A call of qk_rope_forward checks seven tensors; in Python that
+// took 2.4 of the 7.2 us that the call costs the host.
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -60,23 +60,47 @@ PyObject* check(PyObject* const* args, Py_ssize_t n) {
     return PyLong_FromVoidPtr(p);
 }
 
+// on_device(device, t, what, dtype, shape, strides): the same, for a tensor on
+// the GPU of that number.
+PyObject* check_on(PyObject* const* args, Py_ssize_t n) {
+    const int64_t device = n == 6 ? PyLong_AsLongLong(args[0]) : -1;
+    if (device < 0) {
+        if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, "on_device(device, t, what, dtype, shape, strides)");
+        return nullptr;
+    }
+    PyObject* p = check(args + 1, 5);
+    if (!p || args[1] == Py_None) return p;
+    const at::Tensor& t = THPVariable_Unpack(args[1]);
+    if (t.get_device() == device) return p;
+    Py_DECREF(p);
+    return PyErr_Format(PyExc_ValueError, "%U: on %s, the call runs on cuda:%lld", args[2], t.device().str().c_str(),
+                        (long long)device);
+}
+
 // torch throws where a tensor has no plain sizes, strides or memory (symbolic
 // sizes, a tensor under vmap); from a C entry that would end the process.
-PyObject* tensor(PyObject*, PyObject* const* args, Py_ssize_t n) {
+PyObject* guarded(PyObject* (*f)(PyObject* const*, Py_ssize_t), PyObject* const* args, Py_ssize_t n, PyObject* what) {
     try {
-        return check(args, n);
+        return f(args, n);
     } catch (python_error& e) {
         e.restore();
         return nullptr;
     } catch (const c10::Error& e) {
-        return PyErr_Format(PyExc_TypeError, "%S: %s", args[1], e.what_without_backtrace());
+        return PyErr_Format(PyExc_TypeError, "%S: %s", what, e.what_without_backtrace());
     } catch (const std::exception& e) {
-        return PyErr_Format(PyExc_RuntimeError, "%S: %s", args[1], e.what());
+        return PyErr_Format(PyExc_RuntimeError, "%S: %s", what, e.what());
     }
+}
+
+PyObject* tensor(PyObject*, PyObject* const* args, Py_ssize_t n) { return guarded(check, args, n, n > 1 ? args[1] : Py_None); }
+PyObject* on_device(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded(check_on, args, n, n > 2 ? args[2] : Py_None);
 }
 
 PyMethodDef methods[] = {{"tensor", (PyCFunction)(void (*)())tensor, METH_FASTCALL,
                           "tensor(t, what, dtype, shape, strides) -> device pointer"},
+                         {"on_device", (PyCFunction)(void (*)())on_device, METH_FASTCALL,
+                          "on_device(device, t, what, dtype, shape, strides) -> device pointer"},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
