@@ -142,8 +142,13 @@ PagedArgs paged_args(const paged_attention_params_t& p, int64_t tokens, int64_t 
     PagedArgs a;
     memset(&a, 0, sizeof(a));
     a.q_s = p.q_stride; a.o_s = p.out_stride;
-    a.k_s = page_strides(p.k_page_strides); a.v_s = page_strides(p.v_page_strides);
-    a.s_s = page_strides(p.scale_strides);
+    const int64_t cs = cache_elem_size(p.cache_dtype), unit = p.cache_dtype == KV_CACHE_E4M3 ? 8 : 16;
+    const auto units = [&](const int64_t* s, int64_t size, int64_t per) {
+        return PageUnits{(uint32_t)(s[0] * size / per), (uint32_t)(s[1] * size / per)};
+    };
+    a.k_u = units(p.k_page_strides, cs, unit); a.v_u = units(p.v_page_strides, cs, unit);
+    a.s_u = units(p.scale_strides, 1, 1);
+    a.k_head = p.k_page_strides[2] * cs; a.v_head = p.v_page_strides[2] * cs; a.s_head = p.scale_strides[2];
     a.tokens = (int32_t)tokens; a.batch = (int32_t)batch;
     a.max_pages = (int32_t)max_pages; a.n_pages = (int32_t)n_pages;
     a.heads_q = p.heads_q; a.heads_kv = p.heads_kv; a.group = p.heads_q / p.heads_kv; a.d = p.head_dim;
@@ -346,6 +351,9 @@ conv_status_t paged_attention_workspace_bytes(paged_attention_desc_t d, int64_t 
     const conv_status_t st = check_paged_sizes(d->p, tokens, batch, max_pages);
     if (st != CONV_OK) return st;
     *bytes = 0;
+    if (tokens == 0 || batch == 0) return ok();
+    const PagedArgs a = paged_args(d->p, tokens, batch, max_pages, 0);
+    *bytes = plan_paged_attention(d->p.dtype, d->p.cache_dtype == KV_CACHE_E4M3, a).ws_bytes;
     return ok();
 }
 
@@ -380,7 +388,11 @@ conv_status_t paged_attention_forward(paged_attention_desc_t d, int64_t tokens, 
             return fail(CONV_ERR_UNSUPPORTED, "pages reach beyond 2^32 units of %d bytes", (int)unit);
     }
     PagedArgs a = paged_args(p, tokens, batch, max_pages, n_pages);
+    const PagedPlan plan = plan_paged_attention(p.dtype, e4m3, a);
+    if (plan.ws_bytes > 0 && (!workspace || workspace_bytes < plan.ws_bytes))
+        return fail(CONV_ERR_INVALID_ARG, "a workspace of %lld bytes is needed", (long long)plan.ws_bytes);
     if (n_pages == 0) a.max_pages = 0;   // no key to see
+    const View wv = flat_view(workspace, plan.ws_bytes);
     const View ov = rows_view(out, tokens, p.out_stride, p.heads_q * hd, es);
     const View in[8] = {rows_view(q, tokens, p.q_stride, p.heads_q * hd, es),
                         flat_view(q_offsets, 4 * (batch + 1)),
@@ -390,14 +402,17 @@ conv_status_t paged_attention_forward(paged_attention_desc_t d, int64_t tokens, 
                         pages_view(v_pages, p.v_page_strides, n_pages, ps, h, hd, cs),
                         pages_view(e4m3 ? k_scales : nullptr, p.scale_strides, n_pages, ps, h, 1, 1),
                         pages_view(e4m3 ? v_scales : nullptr, p.scale_strides, n_pages, ps, h, 1, 1)};
+    if (views_overlap(ov, wv)) return fail(CONV_ERR_ALIAS, "out overlaps the workspace");
     for (const View& iv : in)
-        if (views_overlap(ov, iv)) return fail(CONV_ERR_ALIAS, "out overlaps an input");
+        if (views_overlap(ov, iv) || views_overlap(wv, iv))
+            return fail(CONV_ERR_ALIAS, "out or the workspace overlaps an input");
     a.q = q; a.out = out; a.q_offsets = q_offsets; a.kv_lens = kv_lens; a.page_table = page_table;
     a.k = k_pages; a.v = v_pages;
     a.ks = e4m3 ? k_scales : nullptr;
     a.vs = e4m3 ? v_scales : nullptr;
-    (void)workspace_bytes;
-    return hip_status(launch_paged_attention(p.dtype, e4m3, a, (hipStream_t)stream), "paged_attention");
+    a.ws = plan.ws_bytes > 0 ? workspace : nullptr;
+    a.tiles = plan.tiles; a.parts = plan.parts;
+    return hip_status(launch_paged_attention(p.dtype, e4m3, plan, a, (hipStream_t)stream), "paged_attention");
 }
 
 // --------------------------------------------------------- block norm ----

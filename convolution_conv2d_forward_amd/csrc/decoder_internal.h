@@ -39,6 +39,12 @@ hipError_t launch_kv_load(int32_t dtype, bool e4m3, bool vec, const KvArgs& a, h
 
 // ---------------------------------------------------- paged attention ----
 
+// Strides of pages in units of 16 bytes (E4M3: of 8), modulo 2^32: a page's
+// and token's place is formed in 32 bits, since pages reach less far.
+struct PageUnits {
+    uint32_t page, token;
+};
+
 struct PagedArgs {
     const void* q;
     const void* k;               // pages
@@ -49,16 +55,29 @@ struct PagedArgs {
     const int32_t* q_offsets;
     const int32_t* kv_lens;
     const int32_t* page_table;
+    void* ws;                    // null when parts == 0
     int64_t q_s, o_s;            // token strides
-    PageStrides k_s, v_s, s_s;
+    int64_t k_head, v_head;      // head strides of the pages, bytes
+    PageUnits k_u, v_u, s_u;     // s_u in bytes
+    int64_t s_head;
     int32_t tokens, batch, max_pages, n_pages;
     int32_t heads_q, heads_kv, group, d;
     int32_t window, sinks;
     DivU32 page_size;
+    int32_t tiles;               // row tiles of all sequences, at most
+    int32_t first_tile;          // of this launch, where parts == 0
+    int32_t parts;               // workgroups that the keys of all tiles are divided among, at most; 0: one a tile and head
     float scale, softcap;
 };
 
-hipError_t launch_paged_attention(int32_t dtype, bool e4m3, const PagedArgs& a, hipStream_t s);
+// Workgroups and workspace that a call of these sizes runs with.
+struct PagedPlan {
+    int32_t tiles, parts;
+    int64_t ws_bytes;
+};
+
+PagedPlan plan_paged_attention(int32_t dtype, bool e4m3, const PagedArgs& a);
+hipError_t launch_paged_attention(int32_t dtype, bool e4m3, const PagedPlan& p, const PagedArgs& a, hipStream_t s);
 
 // --------------------------------------------------------- block norm ----
 

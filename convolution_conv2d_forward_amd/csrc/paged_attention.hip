@@ -1,95 +1,202 @@
-// Softmax attention of new tokens over the pages of a cache.
-#include "attention_common.h"
-#include "decoder_internal.h"
-#include "e4m3.h"
+// Dispatch of paged_attention_forward, and the join of divided results.
+#include "linear_common.h"
+#include "paged_common.h"
 
 namespace conv2d {
 
 namespace {
 
-// A wave a (new token, head): a key at a time, a lane every 64th element.
-template <typename T, bool E4>
-__global__ __launch_bounds__(256) void paged_any(PagedArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t all = (int64_t)a.tokens * a.heads_q;
-    for (int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); w < all; w += (int64_t)gridDim.x * 4) {
-        const int t = (int)(w / a.heads_q), hq = (int)(w - (int64_t)t * a.heads_q), hk = hq / a.group;
-        // The last sequence that starts at or before t.
-        int b = 0, end = a.batch + 1;
-        while (b < end) {
-            const int mid = (b + end) >> 1;
-            if (a.q_offsets[mid] <= t)
-                b = mid + 1;
-            else
-                end = mid;
-        }
-        --b;
-        if (b < 0 || b >= a.batch) continue;
-        const int first = max(a.q_offsets[b], 0), nq = min(a.q_offsets[b + 1], a.tokens) - first;
-        const int nk = min(max(a.kv_lens[b], 0), a.max_pages * (int)a.page_size.d);
-        if (t - first >= nq) continue;
-        const int p = nk - nq + (t - first);
-        float q[4], o[4] = {};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            q[i] = lane + 64 * i < a.d ? to_f32(((const T*)a.q)[t * a.q_s + (int64_t)hq * a.d + lane + 64 * i]) : 0.0f;
-        float top = -INFINITY, total = 0.0f;
-        for (int j = 0; j <= p; ++j) {
-            if (a.window && p - j >= a.window && j >= a.sinks) {
-                j = p - a.window;
-                continue;
-            }
-            const uint32_t n = divu((uint32_t)j, a.page_size), token = (uint32_t)j - n * a.page_size.d;
-            const int page = a.page_table[(int64_t)b * a.max_pages + n];
-            if (page < 0 || page >= a.n_pages) continue;
-            const auto row = [&](const void* pages, const PageStrides& s, const uint8_t* scales, float (&x)[4]) {
-                const int64_t at = page * s.page + (int64_t)token * s.token + hk * s.head;
-                float scale = 1.0f;
-                if (E4) scale = scale_value(scales[page * a.s_s.page + (int64_t)token * a.s_s.token + hk * a.s_s.head]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int e = lane + 64 * i;
-                    x[i] = 0.0f;
-                    if (e < a.d) x[i] = E4 ? decode1(((const uint8_t*)pages)[at + e], scale) : to_f32(((const T*)pages)[at + e]);
-                }
-            };
-            float x[4], dot[1] = {0.0f};
-            row(a.k, a.k_s, a.ks, x);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dot[0] += q[i] * x[i];
-#pragma unroll
-            for (int m = 1; m < 64; m <<= 1) dot[0] += __shfl_xor(dot[0], m, 64);
-            ScoreP sp;
-            sp.cap = a.softcap;
-            sp.scale = a.softcap > 0.0f ? cap_scale(a.scale, a.softcap) : a.scale * kLog2e;
-            scores<T>(sp, dot);
-            const float now = fmaxf(top, dot[0]), fade = __builtin_amdgcn_exp2f(top - (now == -INFINITY ? 0.0f : now));
-            const float weight = __builtin_amdgcn_exp2f(dot[0] - (now == -INFINITY ? 0.0f : now));
-            top = now;
-            total = total * fade + weight;
-            row(a.v, a.v_s, a.vs, x);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = o[i] * fade + weight * x[i];
-        }
-        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (lane + 64 * i < a.d) ((T*)a.out)[t * a.o_s + (int64_t)hq * a.d + lane + 64 * i] = from_f32<T>(o[i] * inv);
-    }
+// The results of a (tile, head): `n` of them, the first in `slot0` of the
+// workspace, the others in every second one from `slot1` on.
+struct Results {
+    int n, slot0, slot1;
+    __device__ __forceinline__ int slot(int i) const { return i == 0 ? slot0 : slot1 + 2 * i; }
+};
+__device__ __forceinline__ Results results_of(const PagedArgs& a, const PagedWs& w, int t, int h) {
+    const int all = w.head[1], parts = w.head[2], c = w.cum[t], n = w.cum[t + 1] - c;
+    const int begin = c * a.heads_kv + h * n, first = part_of(all, parts, begin), last = part_of(all, parts, begin + n - 1);
+    return Results{last - first + 1, 2 * first + (part_begin(all, parts, first) != begin), 2 * first};
 }
 
-template <typename T, bool E4>
-hipError_t run(const PagedArgs& a, hipStream_t s) {
-    const int64_t most = (int64_t)device_cu_count() * 64, n = ((int64_t)a.tokens * a.heads_q + 3) / 4;
-    paged_any<T, E4><<<dim3((uint32_t)(n < most ? n : most)), dim3(256), 0, s>>>(a);
+// Where a row's outputs go; false if the row is none.
+template <typename T, int R>
+__device__ __forceinline__ bool out_row(const PagedArgs& a, const PagedWs& w, int t, int h, int r, T*& out) {
+    const PagedSeq s = paged_seq(a, w.seq[t]);
+    const int row = w.tile[t] * R + r;
+    if (row >= s.nq * a.group) return false;
+    const int qi = row / a.group, hq = h * a.group + row - qi * a.group;
+    out = (T*)a.out + (int64_t)(s.first + qi) * a.o_s + (int64_t)hq * a.d;
+    return true;
+}
+
+// Few results: as many threads as a row is wide add up its outputs.
+template <typename T, int R, int DP>
+__global__ __launch_bounds__(256) void paged_join_few(PagedArgs a) {
+    constexpr int W = DP / 4;
+    const uint32_t at = blockIdx.x * (256 / W) + threadIdx.x / W;
+    const int e = (threadIdx.x % W) * 4, r = (int)(at % R), h = (int)(at / R % (uint32_t)a.heads_kv);
+    const int t = (int)(at / R / (uint32_t)a.heads_kv);
+    const PagedWs w = paged_ws<R>(a);
+    if (t >= w.head[0] || e >= a.d) return;
+    const Results res = results_of(a, w, t, h);
+    T* out;
+    if (res.n == 1 || !out_row<T, R>(a, w, t, h, r, out)) return;   // one: written whole
+    float top = -INFINITY, l = 0.0f;
+    f32x4 sum{0, 0, 0, 0};
+    for (int s0 = 0; s0 < res.n; s0 += 4) {
+        f32x2 st[4];
+        f32x4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t row = (int64_t)res.slot(min(s0 + i, res.n - 1)) * R + r;
+            st[i] = w.stat[row];
+            v[i] = *(const f32x4*)(w.out + row * a.d + e);
+            if (s0 + i >= res.n) st[i] = f32x2{-INFINITY, 0.0f};
+        }
+        float m = top;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = fmaxf(m, st[i][0]);
+        const float base = m == -INFINITY ? 0.0f : m, fade = __builtin_amdgcn_exp2f(top - base);
+        top = m;
+        l *= fade;
+        sum *= fade;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float f = __builtin_amdgcn_exp2f(st[i][0] - base);
+            l += f * st[i][1];
+            if (s0 + i < res.n) sum += v[i] * f;
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    *(typename Vec<T>::v4*)(out + e) = from_f32<T>(sum * inv);
+}
+
+// Many: a workgroup a row.  The results' maxima and sums give each one's
+// factor; then groups of threads, each as wide as the row, add up the outputs
+// of every GROUPS-th result, four loads in flight, and meet in LDS.
+constexpr int kMostParts = 1024;
+template <typename T, int R, int DP>
+__global__ __launch_bounds__(256) void paged_join_many(PagedArgs a) {
+    constexpr int W = DP / 4, GROUPS = 256 / W;
+    __shared__ float top_w[4], sum_w[4], factor[kMostParts];
+    __shared__ __align__(16) f32x4 part[GROUPS][W];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int r = (int)(blockIdx.x % R), h = (int)(blockIdx.x / R % (uint32_t)a.heads_kv);
+    const int t = (int)(blockIdx.x / R / (uint32_t)a.heads_kv);
+    const PagedWs w = paged_ws<R>(a);
+    if (t >= w.head[0]) return;
+    const Results res = results_of(a, w, t, h);
+    T* out;
+    if (res.n == 1 || !out_row<T, R>(a, w, t, h, r, out)) return;   // one: written whole
+    f32x2 st[kMostParts / 256];
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kMostParts / 256; ++i) {
+        st[i] = f32x2{-INFINITY, 0.0f};
+        if (tid + 256 * i < res.n) st[i] = w.stat[(int64_t)res.slot(tid + 256 * i) * R + r];
+        top = fmaxf(top, st[i][0]);
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m, 64));
+    if (lane == 0) top_w[wave] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(top_w[0], top_w[1]), fmaxf(top_w[2], top_w[3]));
+    float l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMostParts / 256; ++i) {
+        const float f = __builtin_amdgcn_exp2f(st[i][0] - (top == -INFINITY ? 0.0f : top));
+        factor[tid + 256 * i] = f;
+        l += f * st[i][1];
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) l += __shfl_xor(l, m, 64);
+    if (lane == 0) sum_w[wave] = l;
+    __syncthreads();
+    l = sum_w[0] + sum_w[1] + sum_w[2] + sum_w[3];
+    const int grp = tid / W, e = (tid % W) * 4;
+    f32x4 sum{0, 0, 0, 0};
+    for (int s0 = grp; s0 < res.n; s0 += 4 * GROUPS) {
+        f32x4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s = s0 + i * GROUPS;
+            v[i] = f32x4{0, 0, 0, 0};
+            if (s < res.n && e < a.d) v[i] = *(const f32x4*)(w.out + ((int64_t)res.slot(s) * R + r) * a.d + e);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s = s0 + i * GROUPS;
+            if (s < res.n) sum += v[i] * factor[s];
+        }
+    }
+    part[grp][tid % W] = sum;
+    __syncthreads();
+    if (grp != 0 || e >= a.d) return;
+#pragma unroll
+    for (int i = 1; i < GROUPS; ++i) sum += part[i][tid];
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    *(typename Vec<T>::v4*)(out + e) = from_f32<T>(sum * inv);
+}
+
+template <typename T, int R, int DP>
+hipError_t join(const PagedArgs& a, hipStream_t s) {
+    const int64_t units = (int64_t)a.tiles * a.heads_kv;
+    if (a.parts >= 8 * units) {
+        paged_join_many<T, R, DP><<<dim3((uint32_t)(units * R)), dim3(256), 0, s>>>(a);
+    } else {
+        constexpr int rows = 256 / (DP / 4);
+        paged_join_few<T, R, DP><<<dim3((uint32_t)((units * R + rows - 1) / rows)), dim3(256), 0, s>>>(a);
+    }
     return hipGetLastError();
+}
+
+template <typename T, int R>
+hipError_t join(const PagedArgs& a, hipStream_t s) {
+    if (a.d <= 64) return join<T, R, 64>(a, s);
+    if (a.d <= 128) return join<T, R, 128>(a, s);
+    return join<T, R, 256>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_paged_attention(int32_t dtype, bool e4m3, const PagedArgs& a, hipStream_t s) {
-    if (dtype == CONV_DTYPE_F32) return e4m3 ? run<float, true>(a, s) : run<float, false>(a, s);
-    return e4m3 ? run<bf16, true>(a, s) : run<bf16, false>(a, s);
+PagedPlan plan_paged_attention(int32_t dtype, bool e4m3, const PagedArgs& a) {
+    PagedPlan p{};
+    constexpr int R = 16;
+    const int64_t seqs = a.batch < a.tokens ? a.batch : a.tokens;
+    p.tiles = (int32_t)(((int64_t)a.tokens * a.group + seqs * (R - 1)) / R);
+    const int size = dtype == CONV_DTYPE_F32 ? 4 : 2, dp = a.d <= 64 ? 64 : a.d <= 128 ? 128 : 256;
+    const int64_t wgs = (int64_t)device_cu_count() * (dp * size <= 256 ? 2 : 1);
+    const int64_t units = (int64_t)p.tiles * a.heads_kv, bu = dp * size > 512 ? 64 : 128;
+    const int64_t blocks = ((int64_t)a.max_pages * a.page_size.d + bu - 1) / bu;
+    if (p.tiles <= kPagedTiles && a.batch <= kPagedTiles && blocks > 1 && units < 4 * wgs && units * (blocks + 1) < 0x7fffffff) {
+        p.parts = (int32_t)(wgs < units * blocks ? wgs : units * blocks);
+        if (p.parts > kMostParts) p.parts = kMostParts;
+        p.ws_bytes = line_bytes(p.tiles) + (int64_t)p.parts * 2 * R * (a.d + 2) * 4;
+    }
+    return p;
+}
+
+hipError_t launch_paged_attention(int32_t dtype, bool e4m3, const PagedPlan& p, const PagedArgs& a, hipStream_t s) {
+    const bool f32 = dtype == CONV_DTYPE_F32;
+    const auto launch = [&](const PagedArgs& c) {
+        if (f32) return e4m3 ? launch_paged_rows<float, true>(c, s) : launch_paged_rows<float, false>(c, s);
+        return e4m3 ? launch_paged_rows<bf16, true>(c, s) : launch_paged_rows<bf16, false>(c, s);
+    };
+    if (p.parts) {
+        const hipError_t e = launch(a);
+        if (e != hipSuccess) return e;
+        return f32 ? join<float, 16>(a, s) : join<bf16, 16>(a, s);
+    }
+    // A workgroup a tile and head, as many tiles as a launch's grid holds.
+    const int64_t most = most_workgroups(256) / a.heads_kv;
+    for (int64_t t = 0; t < p.tiles; t += most) {
+        PagedArgs c = a;
+        c.first_tile = (int32_t)t;
+        c.tiles = (int32_t)(p.tiles - t < most ? p.tiles - t : most);
+        const hipError_t e = launch(c);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace conv2d

@@ -1,0 +1,332 @@
+// Device helpers of the paged attention kernels: which rows and keys a
+// workgroup takes, where keys lie, the join of divided results.
+//
+// The rows (new token, head of the group) of a sequence that share a key head
+// are cut into tiles of R rows, the keys that a tile's rows see into blocks of
+// BU keys: the blocks of the first tokens, then those from the window's first
+// key on.  One workgroup takes a (tile, head) whole where there are many; else
+// the blocks of all tiles and heads form one line, tile after tile and head
+// after head, which is cut into equal parts, a workgroup each, whatever the
+// sequences' lengths.  A (tile, head) that a cut divides leaves partial results
+// in the workspace, two at most a workgroup (one that its part begins with, one
+// that it ends with), which a second launch joins.
+//
+// Lengths and offsets come from the device, so both launches work the line out
+// for themselves: the tiles' blocks are summed up by each workgroup of the
+// first, and left in the workspace for the second.
+#pragma once
+
+#include "attention_common.h"
+#include "decoder_internal.h"
+#include "e4m3.h"
+
+namespace conv2d {
+
+// Tiles and sequences that a divided call may have: four a thread.
+constexpr int kPagedTiles = 1024;
+
+struct PagedSeq {
+    int first, nq, nk;   // its rows of q from `first` on, its new and all its tokens
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int b) {
+    PagedSeq s;
+    s.first = min(max(a.q_offsets[b], 0), a.tokens);
+    s.nq = max(min(max(a.q_offsets[b + 1], 0), a.tokens) - s.first, 0);
+    s.nk = min(max(a.kv_lens[b], 0), a.max_pages * (int)a.page_size.d);
+    return s;
+}
+
+// Blocks of BU keys that rows r0 .. r0 + R - 1 of a sequence see.
+struct KeyBlocks {
+    int ns, w0, n;   // ns from the first key on, then n - ns from block w0 on
+    __device__ __forceinline__ int at(int i) const { return i < ns ? i : w0 + i - ns; }
+};
+template <int R, int BU>
+__device__ __forceinline__ KeyBlocks key_blocks(const PagedArgs& a, PagedSeq s, int r0) {
+    const int p0 = s.nk - s.nq + r0 / a.group, p1 = s.nk - s.nq + (min(r0 + R, s.nq * a.group) - 1) / a.group;
+    const int hi = min(p1 + 1, s.nk), lo = a.window && p0 >= a.window ? p0 - a.window + 1 : 0;
+    KeyBlocks k{0, 0, 0};
+    if (hi <= 0) return k;
+    if (a.window) k.ns = (min(a.sinks, hi) + BU - 1) / BU;
+    k.w0 = max(lo / BU, k.ns);
+    k.n = max(k.ns, k.ns + (hi + BU - 1) / BU - k.w0);
+    return k;
+}
+
+// The keys that a row sees: j < hi and (j >= lo or j < a.sinks).
+__device__ __forceinline__ void paged_interval(const PagedArgs& a, PagedSeq s, int i, bool live, int& lo, int& hi) {
+    const int p = s.nk - s.nq + i;
+    hi = live ? max(p + 1, 0) : 0;   // p < nk
+    lo = a.window && p >= a.window ? p - a.window + 1 : 0;
+}
+
+// Sums of v over the threads before this one of a workgroup of 256, and over
+// all; `part` is read until the next barrier but one.
+template <typename N>
+__device__ __forceinline__ N sum_before(N v, N& all, N* part) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    N s = v;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const N o = __shfl_up(s, m, 64);
+        if (lane >= m) s += o;
+    }
+    __syncthreads();
+    if (lane == 63) part[wave] = s;
+    __syncthreads();
+    all = part[0] + part[1] + part[2] + part[3];
+    N before = s - v;
+    for (int w = 0; w < wave; ++w) before += part[w];
+    return before;
+}
+
+template <int R>
+__device__ __forceinline__ int tiles_of(const PagedArgs& a, int b) {
+    return b < a.batch ? (paged_seq(a, b).nq * a.group + R - 1) / R : 0;
+}
+
+// The line of blocks of a divided call, in LDS.
+struct PagedLine {
+    int first[kPagedTiles + 1];   // a sequence's first tile
+    int cum[kPagedTiles + 1];     // blocks of one head before a tile
+    int part[4];
+    int64_t part64[4];
+};
+
+// The last i of 0 .. n - 1 with t[i] <= x, t ascending from t[0] <= x.
+template <typename F>
+__device__ __forceinline__ int last_at_most(int n, F t, int x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t(mid) <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// Fills the line; returns the number of tiles.  A tile without keys counts a
+// block: its rows are zeros that someone has to write.  Offsets that do not
+// ascend may make more tiles than the host has counted: those are left out.
+template <int R, int BU>
+__device__ __forceinline__ int make_line(const PagedArgs& a, PagedLine& l) {
+    const int tid = threadIdx.x;
+    int n[4], sum = 0, all;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        n[i] = min(tiles_of<R>(a, 4 * tid + i), a.tiles);
+        sum += n[i];
+    }
+    int at = sum_before(sum, all, l.part);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        l.first[4 * tid + i] = at;
+        at += n[i];
+    }
+    const int tiles = min(all, a.tiles);
+    __syncthreads();
+    sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = 4 * tid + i;
+        n[i] = 0;
+        if (t < tiles) {
+            const int b = last_at_most(a.batch, [&](int j) { return l.first[j]; }, t);
+            n[i] = max(key_blocks<R, BU>(a, paged_seq(a, b), (t - l.first[b]) * R).n, 1);
+        }
+        sum += n[i];
+    }
+    at = sum_before(sum, all, l.part);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        l.cum[4 * tid + i] = at;
+        at += n[i];
+    }
+    if (tid == 255) l.cum[kPagedTiles] = at;
+    __syncthreads();
+    return tiles;
+}
+
+// Tile i of the call where each is taken whole: its sequence and its place
+// among the sequence's tiles; false past the last one.
+template <int R>
+__device__ __forceinline__ bool find_tile(const PagedArgs& a, int64_t i, int& b, int& t, int64_t* part) {
+    __shared__ int found[2];
+    const int tid = threadIdx.x;
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 1024) {
+        int64_t n[4], sum = 0, all;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            n[j] = tiles_of<R>(a, b0 + 4 * tid + j);
+            sum += n[j];
+        }
+        int64_t at = before + sum_before(sum, all, part);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (i >= at && i < at + n[j]) {
+                found[0] = b0 + 4 * tid + j;
+                found[1] = (int)(i - at);
+            }
+            at += n[j];
+        }
+        before += all;
+        if (i < before) {
+            __syncthreads();
+            b = __builtin_amdgcn_readfirstlane(found[0]);
+            t = __builtin_amdgcn_readfirstlane(found[1]);
+            return true;
+        }
+    }
+    return false;
+}
+
+// Parts that a line of `all` blocks (all heads) is cut into, and the first
+// block of one.  Each has `least` blocks or more.
+__device__ __forceinline__ int line_parts(const PagedArgs& a, int all, int least) {
+    return max(min(a.parts, all / least), 1);
+}
+__device__ __forceinline__ int part_begin(int all, int parts, int w) { return (int)((int64_t)all * w / parts); }
+__device__ __forceinline__ int part_of(int all, int parts, int block) {
+    return (int)((((int64_t)block + 1) * parts - 1) / all);
+}
+
+// The workspace: the line (tiles, blocks of all heads, parts, then cum and the
+// tiles' sequences and places), then the parts' outputs, R rows of d for each of
+// two results, then their (running maximum, sum).
+struct PagedWs {
+    int32_t* head;
+    int32_t *cum, *seq, *tile;
+    float* out;
+    f32x2* stat;
+};
+__host__ __device__ __forceinline__ int64_t line_bytes(int tiles) { return (int64_t)(4 + 3 * (tiles + 1)) * 4 / 16 * 16 + 16; }
+template <int R>
+__device__ __forceinline__ PagedWs paged_ws(const PagedArgs& a) {
+    PagedWs w;
+    w.head = (int32_t*)a.ws;
+    w.cum = w.head + 4;
+    w.seq = w.cum + a.tiles + 1;
+    w.tile = w.seq + a.tiles + 1;
+    w.out = (float*)((char*)a.ws + line_bytes(a.tiles));
+    w.stat = (f32x2*)(w.out + (int64_t)a.parts * 2 * R * a.d);
+    return w;
+}
+
+// Leaves the line for the join (one workgroup does).
+__device__ __forceinline__ void keep_line(const PagedArgs& a, const PagedLine& l, PagedWs w, int tiles, int all, int parts) {
+    if (threadIdx.x == 0) {
+        w.head[0] = tiles;
+        w.head[1] = all;
+        w.head[2] = parts;
+    }
+    for (int t = threadIdx.x; t <= tiles; t += 256) {
+        w.cum[t] = l.cum[t];
+        if (t < tiles) {
+            const int b = last_at_most(a.batch, [&](int j) { return l.first[j]; }, t);
+            w.seq[t] = b;
+            w.tile[t] = t - l.first[b];
+        }
+    }
+}
+
+// The pieces of a workgroup: blocks k0 .. k1 - 1 of a (tile, head).
+struct Piece {
+    int b, t, h;    // sequence, tile of it, head
+    int k0, k1;
+    int result;     // in the workspace; -1 where the piece is all of its (tile, head)
+};
+struct Pieces {
+    int begin, u, end, tiles, w;
+
+    // `least`: blocks of a part at least.  False: nothing to do.
+    template <int R, int BU>
+    __device__ __forceinline__ bool start(const PagedArgs& a, int least, PagedLine& l) {
+        if (!a.parts) {
+            u = 0;
+            end = 1;
+            return true;
+        }
+        tiles = make_line<R, BU>(a, l);
+        const int all = l.cum[tiles] * a.heads_kv, parts = line_parts(a, all, least);
+        if (blockIdx.x == 0) keep_line(a, l, paged_ws<R>(a), tiles, all, parts);
+        w = (int)xcd_remap(blockIdx.x, (uint32_t)parts);
+        begin = u = __builtin_amdgcn_readfirstlane(part_begin(all, parts, w));
+        end = __builtin_amdgcn_readfirstlane(part_begin(all, parts, w + 1));
+        return (int)blockIdx.x < parts;
+    }
+    template <int R, int BU>
+    __device__ __forceinline__ bool next(const PagedArgs& a, PagedLine& l, Piece& p) {
+        if (u >= end) return false;
+        if (!a.parts) {
+            p.h = (int)(blockIdx.x % (uint32_t)a.heads_kv);
+            if (!find_tile<R>(a, (int64_t)a.first_tile + blockIdx.x / (uint32_t)a.heads_kv, p.b, p.t, l.part64)) return false;
+            p.k0 = 0;
+            p.k1 = key_blocks<R, BU>(a, paged_seq(a, p.b), p.t * R).n;
+            p.result = -1;
+            u = end;
+            return true;
+        }
+        const int heads = a.heads_kv;
+        const int t = __builtin_amdgcn_readfirstlane(last_at_most(tiles, [&](int j) { return l.cum[j] * heads; }, u));
+        const int c = __builtin_amdgcn_readfirstlane(l.cum[t]), n = __builtin_amdgcn_readfirstlane(l.cum[t + 1]) - c;
+        p.b = __builtin_amdgcn_readfirstlane(last_at_most(a.batch, [&](int j) { return l.first[j]; }, t));
+        p.t = t - __builtin_amdgcn_readfirstlane(l.first[p.b]);
+        p.h = (u - c * heads) / n;
+        p.k0 = u - c * heads - p.h * n;
+        p.k1 = min(n, p.k0 + end - u);
+        p.result = p.k0 == 0 && p.k1 == n ? -1 : 2 * w + (u != begin);
+        u += p.k1 - p.k0;
+        return true;
+    }
+};
+
+__device__ __forceinline__ uint32_t from_lane(uint32_t v, int lane) {
+    return (uint32_t)__builtin_amdgcn_ds_bpermute(lane * 4, (int)v);
+}
+
+// Where this lane's key of a tile lies.
+struct KeyPlace {
+    uint32_t k, v, s;   // units from a head's first page; bytes for scales
+    bool there;         // before nk, on a page of the cache
+};
+// Entry of the page table for a key (any number), to be read well before place().
+__device__ __forceinline__ int page_entry(const PagedArgs& a, const int32_t* table, int key) {
+    const int n = (int)divu((uint32_t)key, a.page_size);
+    return table[min(n, a.max_pages - 1)];
+}
+__device__ __forceinline__ KeyPlace key_place(const PagedArgs& a, int entry, int key, int nk) {
+    const uint32_t token = (uint32_t)key - divu((uint32_t)key, a.page_size) * a.page_size.d;
+    KeyPlace p;
+    p.there = key < nk && (uint32_t)entry < (uint32_t)a.n_pages;
+    const uint32_t page = p.there ? (uint32_t)entry : 0, tok = p.there ? token : 0;
+    p.k = page * a.k_u.page + tok * a.k_u.token;
+    p.v = page * a.v_u.page + tok * a.v_u.token;
+    p.s = page * a.s_u.page + tok * a.s_u.token;
+    return p;
+}
+
+// One element of a key's value, for the few that need it alone.
+template <typename T, bool E4>
+__device__ __forceinline__ float value_at(const PagedArgs& a, const int32_t* table, int h, int key, int e) {
+    const KeyPlace p = key_place(a, page_entry(a, table, key), key, INT32_MAX);
+    const char* row = (const char*)a.v + (uint64_t)p.v * (E4 ? 8 : 16) + h * a.v_head;
+    if (E4) return decode1(((const uint8_t*)row)[e], scale_value(a.vs[p.s + h * a.s_head]));
+    return to_f32(((const T*)row)[e]);
+}
+
+template <typename T, bool E4>
+hipError_t launch_paged_rows(const PagedArgs& a, hipStream_t s);
+template <>
+hipError_t launch_paged_rows<float, false>(const PagedArgs& a, hipStream_t s);
+template <>
+hipError_t launch_paged_rows<float, true>(const PagedArgs& a, hipStream_t s);
+template <>
+hipError_t launch_paged_rows<bf16, false>(const PagedArgs& a, hipStream_t s);
+template <>
+hipError_t launch_paged_rows<bf16, true>(const PagedArgs& a, hipStream_t s);
+
+}  // namespace conv2d
