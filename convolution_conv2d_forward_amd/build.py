@@ -25,7 +25,8 @@ SOURCES = ["conv2d_api.cpp", "igemm_f32.hip", "igemm_bf16.hip", "depthwise.hip",
            "attention_api.cpp", "linear.hip", "linear_rows.hip", "linear_f32.hip", "linear_bf16.hip", "qk_rope.hip",
            "attention_any.hip", "attention_f32.hip", "attention_bf16.hip", "attention_rows.hip", "decoder_api.cpp",
            "kv_cache.hip", "block_norm.hip", "paged_attention.hip", "paged_rows_f32.hip", "paged_rows_f32_e4m3.hip",
-           "paged_rows_bf16.hip", "paged_rows_bf16_e4m3.hip"]
+           "paged_rows_bf16.hip", "paged_rows_bf16_e4m3.hip", "paged_tile_f32.hip", "paged_tile_f32_e4m3.hip",
+           "paged_tile_bf16.hip", "paged_tile_bf16_e4m3.hip"]
 
 FLAGS = ["-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC", "-fvisibility=hidden", "-Wall", "-Wno-unused-function",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

@@ -72,6 +72,7 @@ struct PagedArgs {
 
 // Workgroups and workspace that a call of these sizes runs with.
 struct PagedPlan {
+    int32_t rows;                // of a tile: 16, 64 or 128
     int32_t tiles, parts;
     int64_t ws_bytes;
 };

@@ -161,31 +161,55 @@ hipError_t join(const PagedArgs& a, hipStream_t s) {
 
 PagedPlan plan_paged_attention(int32_t dtype, bool e4m3, const PagedArgs& a) {
     PagedPlan p{};
-    constexpr int R = 16;
-    const int64_t seqs = a.batch < a.tokens ? a.batch : a.tokens;
-    p.tiles = (int32_t)(((int64_t)a.tokens * a.group + seqs * (R - 1)) / R);
-    const int size = dtype == CONV_DTYPE_F32 ? 4 : 2, dp = a.d <= 64 ? 64 : a.d <= 128 ? 128 : 256;
-    const int64_t wgs = (int64_t)device_cu_count() * (dp * size <= 256 ? 2 : 1);
-    const int64_t units = (int64_t)p.tiles * a.heads_kv, bu = dp * size > 512 ? 64 : 128;
-    const int64_t blocks = ((int64_t)a.max_pages * a.page_size.d + bu - 1) / bu;
+    const bool f32 = dtype == CONV_DTYPE_F32;
+    const int64_t cus = device_cu_count(), all = (int64_t)a.tokens * a.group, seqs = a.batch < a.tokens ? a.batch : a.tokens;
+    p.rows = all <= 16 * seqs ? 16 : all >= 96 * seqs || (f32 && a.d > 128) ? 128 : 64;
+    p.tiles = (int32_t)((all + seqs * (p.rows - 1)) / p.rows);
+    // Workgroups that run at once, and a block's keys: as the kernels have them.
+    const int size = f32 ? 4 : 2, bytes = (a.d <= 64 ? 64 : a.d <= 128 ? 128 : 256) * size;
+    int64_t per_cu, keys;
+    if (p.rows == 16) {
+        per_cu = bytes <= 256 ? 2 : 1;
+        keys = bytes > 512 ? 64 : 128;
+    } else {
+        keys = f32 && p.rows == 128 ? 32 : 64;
+        const int64_t stage = 2 * keys * bytes;
+        per_cu = stage <= 16384 ? 3 : stage <= 32768 ? 2 : 1;
+    }
+    const int64_t wgs = cus * per_cu, units = (int64_t)p.tiles * a.heads_kv;
+    const int64_t blocks = ((int64_t)a.max_pages * a.page_size.d + keys - 1) / keys;
     if (p.tiles <= kPagedTiles && a.batch <= kPagedTiles && blocks > 1 && units < 4 * wgs && units * (blocks + 1) < 0x7fffffff) {
         p.parts = (int32_t)(wgs < units * blocks ? wgs : units * blocks);
         if (p.parts > kMostParts) p.parts = kMostParts;
-        p.ws_bytes = line_bytes(p.tiles) + (int64_t)p.parts * 2 * R * (a.d + 2) * 4;
+        p.ws_bytes = line_bytes(p.tiles) + (int64_t)p.parts * 2 * p.rows * (a.d + 2) * 4;
     }
     return p;
 }
 
+namespace {
+
+template <typename T, bool E4>
+hipError_t launch(const PagedPlan& p, const PagedArgs& a, hipStream_t s) {
+    return p.rows == 16 ? launch_paged_rows<T, E4>(a, s) : launch_paged_tile<T, E4>(a, p.rows, s);
+}
+
+template <typename T>
+hipError_t join(const PagedPlan& p, const PagedArgs& a, hipStream_t s) {
+    return p.rows == 16 ? join<T, 16>(a, s) : p.rows == 64 ? join<T, 64>(a, s) : join<T, 128>(a, s);
+}
+
+}  // namespace
+
 hipError_t launch_paged_attention(int32_t dtype, bool e4m3, const PagedPlan& p, const PagedArgs& a, hipStream_t s) {
     const bool f32 = dtype == CONV_DTYPE_F32;
-    const auto launch = [&](const PagedArgs& c) {
-        if (f32) return e4m3 ? launch_paged_rows<float, true>(c, s) : launch_paged_rows<float, false>(c, s);
-        return e4m3 ? launch_paged_rows<bf16, true>(c, s) : launch_paged_rows<bf16, false>(c, s);
+    const auto run = [&](const PagedArgs& c) {
+        if (f32) return e4m3 ? launch<float, true>(p, c, s) : launch<float, false>(p, c, s);
+        return e4m3 ? launch<bf16, true>(p, c, s) : launch<bf16, false>(p, c, s);
     };
     if (p.parts) {
-        const hipError_t e = launch(a);
+        const hipError_t e = run(a);
         if (e != hipSuccess) return e;
-        return f32 ? join<float, 16>(a, s) : join<bf16, 16>(a, s);
+        return f32 ? join<float>(p, a, s) : join<bf16>(p, a, s);
     }
     // A workgroup a tile and head, as many tiles as a launch's grid holds.
     const int64_t most = most_workgroups(256) / a.heads_kv;
@@ -193,7 +217,7 @@ hipError_t launch_paged_attention(int32_t dtype, bool e4m3, const PagedPlan& p, 
         PagedArgs c = a;
         c.first_tile = (int32_t)t;
         c.tiles = (int32_t)(p.tiles - t < most ? p.tiles - t : most);
-        const hipError_t e = launch(c);
+        const hipError_t e = run(c);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;

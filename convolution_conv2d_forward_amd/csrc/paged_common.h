@@ -318,15 +318,20 @@ __device__ __forceinline__ float value_at(const PagedArgs& a, const int32_t* tab
     return to_f32(((const T*)row)[e]);
 }
 
+// Few rows a tile (paged_rows.h) or 64 or 128 (paged_tile.h).
 template <typename T, bool E4>
 hipError_t launch_paged_rows(const PagedArgs& a, hipStream_t s);
-template <>
-hipError_t launch_paged_rows<float, false>(const PagedArgs& a, hipStream_t s);
-template <>
-hipError_t launch_paged_rows<float, true>(const PagedArgs& a, hipStream_t s);
-template <>
-hipError_t launch_paged_rows<bf16, false>(const PagedArgs& a, hipStream_t s);
-template <>
-hipError_t launch_paged_rows<bf16, true>(const PagedArgs& a, hipStream_t s);
+template <typename T, bool E4>
+hipError_t launch_paged_tile(const PagedArgs& a, int rows, hipStream_t s);
+#define CONV2D_PAGED_LAUNCHES(T, E4)                                 \
+    template <>                                                      \
+    hipError_t launch_paged_rows<T, E4>(const PagedArgs& a, hipStream_t s); \
+    template <>                                                      \
+    hipError_t launch_paged_tile<T, E4>(const PagedArgs& a, int rows, hipStream_t s);
+CONV2D_PAGED_LAUNCHES(float, false)
+CONV2D_PAGED_LAUNCHES(float, true)
+CONV2D_PAGED_LAUNCHES(bf16, false)
+CONV2D_PAGED_LAUNCHES(bf16, true)
+#undef CONV2D_PAGED_LAUNCHES
 
 }  // namespace conv2d

@@ -82,6 +82,13 @@ __device__ __forceinline__ void copy16_to_lds(const void* base, uint32_t off, co
                  : "memory", "m0");
 #endif
 }
+// The same from an address of each lane's own.
+__device__ __forceinline__ void copy16_to_lds(const void* p, const u32x4* lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const uint32_t m = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(m) : "memory", "m0");
+#endif
+}
 // The same for 4 bytes per lane: lane l writes lds + 4 l bytes.
 __device__ __forceinline__ void copy4_to_lds(const void* base, uint32_t off, const u32x4* lds) {
 #if defined(__HIP_DEVICE_COMPILE__)
