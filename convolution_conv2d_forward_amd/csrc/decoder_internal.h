@@ -82,7 +82,7 @@ hipError_t launch_paged_attention(int32_t dtype, bool e4m3, const PagedPlan& p, 
 
 // --------------------------------------------------------- block norm ----
 
-constexpr int32_t NORM_MAX_WIDTH = 32768;   // a row fits in the registers of 1024 threads
+constexpr int32_t NORM_MAX_WIDTH = 32768;   // a row fits in LDS in fp32
 
 struct NormArgs {
     const void* y;
