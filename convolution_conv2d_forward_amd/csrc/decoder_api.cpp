@@ -142,11 +142,11 @@ PagedArgs paged_args(const paged_attention_params_t& p, int64_t tokens, int64_t 
     PagedArgs a;
     memset(&a, 0, sizeof(a));
     a.q_s = p.q_stride; a.o_s = p.out_stride;
-    const int64_t cs = cache_elem_size(p.cache_dtype), unit = p.cache_dtype == KV_CACHE_E4M3 ? 8 : 16;
+    const int64_t cs = cache_elem_size(p.cache_dtype);
     const auto units = [&](const int64_t* s, int64_t size, int64_t per) {
         return PageUnits{(uint32_t)(s[0] * size / per), (uint32_t)(s[1] * size / per)};
     };
-    a.k_u = units(p.k_page_strides, cs, unit); a.v_u = units(p.v_page_strides, cs, unit);
+    a.k_u = units(p.k_page_strides, cs, 16); a.v_u = units(p.v_page_strides, cs, 16);
     a.s_u = units(p.scale_strides, 1, 1);
     a.k_head = p.k_page_strides[2] * cs; a.v_head = p.v_page_strides[2] * cs; a.s_head = p.scale_strides[2];
     a.tokens = (int32_t)tokens; a.batch = (int32_t)batch;
@@ -318,10 +318,10 @@ conv_status_t paged_attention_desc_create(const paged_attention_params_t* pp, pa
     if (p.heads_q % p.heads_kv)
         return fail(CONV_ERR_INCOMPATIBLE_SHAPES, "heads_kv = %d does not divide heads_q = %d", p.heads_kv, p.heads_q);
     if (p.head_dim < 1) return fail(CONV_ERR_INVALID_ARG, "head_dim = %d", p.head_dim);
-    const bool e4m3 = p.cache_dtype == KV_CACHE_E4M3;
-    const int64_t chunk = 16 / elem_size(p.dtype), unit = e4m3 ? 8 : chunk, whole = unit > chunk ? unit : chunk;
-    if (p.head_dim > 256 || p.head_dim % whole)
-        return fail(CONV_ERR_UNSUPPORTED, "head_dim = %d is not a multiple of %d up to 256", p.head_dim, (int)whole);
+    // Elements of 16 bytes of q, and of the pages.
+    const int64_t chunk = 16 / elem_size(p.dtype), unit = 16 / cache_elem_size(p.cache_dtype);
+    if (p.head_dim > 256 || p.head_dim % unit)
+        return fail(CONV_ERR_UNSUPPORTED, "head_dim = %d is not a multiple of %d up to 256", p.head_dim, (int)unit);
     if (p.page_size < 1 || p.page_size > 1 << 16)
         return fail(CONV_ERR_INVALID_ARG, "page_size = %d must be 1 .. 2^16", p.page_size);
     if (p.window < 0 || p.sinks < 0) return fail(CONV_ERR_INVALID_ARG, "window = %d, sinks = %d", p.window, p.sinks);
@@ -374,9 +374,8 @@ conv_status_t paged_attention_forward(paged_attention_desc_t d, int64_t tokens, 
     if (max_pages > 0 && !page_table) return fail(CONV_ERR_INVALID_ARG, "null page_table");
     if (n_pages > 0 && (!k_pages || !v_pages || (e4m3 && (!k_scales || !v_scales))))
         return fail(CONV_ERR_INVALID_ARG, "null pages, or scales of an E4M3 cache");
-    const int64_t unit = e4m3 ? 8 : 16;
-    if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || misaligned(k_pages, unit) || misaligned(v_pages, unit))
-        return fail(CONV_ERR_INVALID_ARG, "a tensor or the workspace is not aligned to 16 bytes (E4M3 pages: 8)");
+    if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || !aligned16(k_pages) || !aligned16(v_pages))
+        return fail(CONV_ERR_INVALID_ARG, "a tensor or the workspace is not aligned to 16 bytes");
     if (misaligned(q_offsets, 4) || misaligned(kv_lens, 4) || misaligned(page_table, 4))
         return fail(CONV_ERR_INVALID_ARG, "q_offsets, kv_lens or page_table is not aligned to 4 bytes");
     const int64_t ps = p.page_size, h = p.heads_kv, hd = p.head_dim, es = elem_size(p.dtype), cs = cache_elem_size(p.cache_dtype);
@@ -384,8 +383,8 @@ conv_status_t paged_attention_forward(paged_attention_desc_t d, int64_t tokens, 
         const auto far = [&](const int64_t* s, int64_t len, int64_t per) {
             return pages_too_far(s, n_pages, ps, h) || pages_span(s, n_pages, ps, h, len) / per >= (int64_t)1 << 32;
         };
-        if (far(p.k_page_strides, hd, unit / cs) || far(p.v_page_strides, hd, unit / cs) || (e4m3 && far(p.scale_strides, 1, 1)))
-            return fail(CONV_ERR_UNSUPPORTED, "pages reach beyond 2^32 units of %d bytes", (int)unit);
+        if (far(p.k_page_strides, hd, 16 / cs) || far(p.v_page_strides, hd, 16 / cs) || (e4m3 && far(p.scale_strides, 1, 1)))
+            return fail(CONV_ERR_UNSUPPORTED, "pages reach beyond 2^36 bytes, or their scales beyond 2^32");
     }
     PagedArgs a = paged_args(p, tokens, batch, max_pages, n_pages);
     const PagedPlan plan = plan_paged_attention(p.dtype, e4m3, a);

@@ -39,8 +39,8 @@ hipError_t launch_kv_load(int32_t dtype, bool e4m3, bool vec, const KvArgs& a, h
 
 // ---------------------------------------------------- paged attention ----
 
-// Strides of pages in units of 16 bytes (E4M3: of 8), modulo 2^32: a page's
-// and token's place is formed in 32 bits, since pages reach less far.
+// Strides of pages in units of 16 bytes, modulo 2^32: a page's and token's place
+// is formed in 32 bits, since pages reach less far.
 struct PageUnits {
     uint32_t page, token;
 };

@@ -1,4 +1,6 @@
 // Dispatch of paged_attention_forward, and the join of divided results.
+#include <numeric>
+
 #include "linear_common.h"
 #include "paged_common.h"
 
@@ -12,21 +14,22 @@ struct Results {
     int n, slot0, slot1;
     __device__ __forceinline__ int slot(int i) const { return i == 0 ? slot0 : slot1 + 2 * i; }
 };
-__device__ __forceinline__ Results results_of(const PagedArgs& a, const PagedWs& w, int t, int h) {
-    const int all = w.head[1], parts = w.head[2], c = w.cum[t], n = w.cum[t + 1] - c;
-    const int begin = c * a.heads_kv + h * n, first = part_of(all, parts, begin), last = part_of(all, parts, begin + n - 1);
-    return Results{last - first + 1, 2 * first + (part_begin(all, parts, first) != begin), 2 * first};
-}
 
-// Where a row's outputs go; false if the row is none.
+// Those of tile t, and where row r of it goes; n = 0 where there is nothing to
+// join: one result was written whole.
 template <typename T, int R>
-__device__ __forceinline__ bool out_row(const PagedArgs& a, const PagedWs& w, int t, int h, int r, T*& out) {
-    const PagedSeq s = paged_seq(a, w.seq[t]);
-    const int row = w.tile[t] * R + r;
-    if (row >= s.nq * a.group) return false;
-    const int qi = row / a.group, hq = h * a.group + row - qi * a.group;
-    out = (T*)a.out + (int64_t)(s.first + qi) * a.o_s + (int64_t)hq * a.d;
-    return true;
+__device__ __forceinline__ Results results_of(const PagedArgs& a, const PagedWs& w, int t, int h, int r, T*& out) {
+    // At once: t is at most the tiles that the line has room for.
+    const int tiles = w.head[0], all = w.head[1], parts = w.head[2], c = w.cum[t], end = w.cum[t + 1];
+    const int first_row = w.first[t], nq = w.nq[t], place = w.tile[t];
+    Results res{0, 0, 0};
+    const int row = place * R + r;
+    if (t >= tiles || row >= nq * a.group) return res;
+    const int qi = row / a.group, hq = h * a.group + row - qi * a.group, n = end - c;
+    out = (T*)a.out + (int64_t)(first_row + qi) * a.o_s + (int64_t)hq * a.d;
+    const int begin = c * a.heads_kv + h * n, first = part_of(all, parts, begin), last = part_of(all, parts, begin + n - 1);
+    if (first == last) return res;
+    return Results{last - first + 1, 2 * first + (part_begin(all, parts, first) != begin), 2 * first};
 }
 
 // Few results: as many threads as a row is wide add up its outputs.
@@ -37,10 +40,10 @@ __global__ __launch_bounds__(256) void paged_join_few(PagedArgs a) {
     const int e = (threadIdx.x % W) * 4, r = (int)(at % R), h = (int)(at / R % (uint32_t)a.heads_kv);
     const int t = (int)(at / R / (uint32_t)a.heads_kv);
     const PagedWs w = paged_ws<R>(a);
-    if (t >= w.head[0] || e >= a.d) return;
-    const Results res = results_of(a, w, t, h);
+    if (t >= a.tiles || e >= a.d) return;
     T* out;
-    if (res.n == 1 || !out_row<T, R>(a, w, t, h, r, out)) return;   // one: written whole
+    const Results res = results_of<T, R>(a, w, t, h, r, out);
+    if (res.n == 0) return;
     float top = -INFINITY, l = 0.0f;
     f32x4 sum{0, 0, 0, 0};
     for (int s0 = 0; s0 < res.n; s0 += 4) {
@@ -84,10 +87,9 @@ __global__ __launch_bounds__(256) void paged_join_many(PagedArgs a) {
     const int r = (int)(blockIdx.x % R), h = (int)(blockIdx.x / R % (uint32_t)a.heads_kv);
     const int t = (int)(blockIdx.x / R / (uint32_t)a.heads_kv);
     const PagedWs w = paged_ws<R>(a);
-    if (t >= w.head[0]) return;
-    const Results res = results_of(a, w, t, h);
     T* out;
-    if (res.n == 1 || !out_row<T, R>(a, w, t, h, r, out)) return;   // one: written whole
+    const Results res = results_of<T, R>(a, w, t, h, r, out);
+    if (res.n == 0) return;
     f32x2 st[kMostParts / 256];
     float top = -INFINITY;
 #pragma unroll
@@ -164,7 +166,9 @@ PagedPlan plan_paged_attention(int32_t dtype, bool e4m3, const PagedArgs& a) {
     const bool f32 = dtype == CONV_DTYPE_F32;
     const int64_t cus = device_cu_count(), all = (int64_t)a.tokens * a.group, seqs = a.batch < a.tokens ? a.batch : a.tokens;
     p.rows = all <= 16 * seqs ? 16 : all >= 96 * seqs || (f32 && a.d > 128) ? 128 : 64;
-    p.tiles = (int32_t)((all + seqs * (p.rows - 1)) / p.rows);
+    // A sequence's rows come in groups: what its last tile may lack is a multiple
+    // of what the group has in common with a tile.
+    p.tiles = (int32_t)((all + seqs * (p.rows - std::gcd(a.group, p.rows))) / p.rows);
     // Workgroups that run at once, and a block's keys: as the kernels have them.
     const int size = f32 ? 4 : 2, bytes = (a.d <= 64 ? 64 : a.d <= 128 ? 128 : 256) * size;
     int64_t per_cu, keys;

@@ -194,87 +194,161 @@ __device__ __forceinline__ int part_of(int all, int parts, int block) {
     return (int)((((int64_t)block + 1) * parts - 1) / all);
 }
 
-// The workspace: the line (tiles, blocks of all heads, parts, then cum and the
-// tiles' sequences and places), then the parts' outputs, R rows of d for each of
+// The workspace: the line (tiles, blocks of all heads, parts, then for each tile
+// the blocks before it, its sequence's first row and rows of q, and its place
+// among the sequence's tiles), then the parts' outputs, R rows of d for each of
 // two results, then their (running maximum, sum).
 struct PagedWs {
     int32_t* head;
-    int32_t *cum, *seq, *tile;
+    int32_t *cum, *first, *nq, *tile;
     float* out;
     f32x2* stat;
 };
-__host__ __device__ __forceinline__ int64_t line_bytes(int tiles) { return (int64_t)(4 + 3 * (tiles + 1)) * 4 / 16 * 16 + 16; }
+__host__ __device__ __forceinline__ int64_t line_bytes(int tiles) { return (int64_t)(4 + 4 * (tiles + 1)) * 4 / 16 * 16 + 16; }
 template <int R>
 __device__ __forceinline__ PagedWs paged_ws(const PagedArgs& a) {
     PagedWs w;
     w.head = (int32_t*)a.ws;
     w.cum = w.head + 4;
-    w.seq = w.cum + a.tiles + 1;
-    w.tile = w.seq + a.tiles + 1;
+    w.first = w.cum + a.tiles + 1;
+    w.nq = w.first + a.tiles + 1;
+    w.tile = w.nq + a.tiles + 1;
     w.out = (float*)((char*)a.ws + line_bytes(a.tiles));
     w.stat = (f32x2*)(w.out + (int64_t)a.parts * 2 * R * a.d);
     return w;
 }
 
-// Leaves the line for the join (one workgroup does).
-__device__ __forceinline__ void keep_line(const PagedArgs& a, const PagedLine& l, PagedWs w, int tiles, int all, int parts) {
-    if (threadIdx.x == 0) {
-        w.head[0] = tiles;
-        w.head[1] = all;
-        w.head[2] = parts;
-    }
-    for (int t = threadIdx.x; t <= tiles; t += 256) {
-        w.cum[t] = l.cum[t];
-        if (t < tiles) {
-            const int b = last_at_most(a.batch, [&](int j) { return l.first[j]; }, t);
-            w.seq[t] = b;
-            w.tile[t] = t - l.first[b];
-        }
-    }
-}
-
 // The pieces of a workgroup: blocks k0 .. k1 - 1 of a (tile, head).
 struct Piece {
+    PagedSeq sq;
     int b, t, h;    // sequence, tile of it, head
     int k0, k1;
     int result;     // in the workspace; -1 where the piece is all of its (tile, head)
 };
+
+// Up to 64 sequences and tiles are kept in the lanes of each wave, a tile a lane:
+// no LDS, no barrier, each length and offset read once (a call of a token of 32
+// sequences: 3 us less than by way of LDS).
+template <int R, int BU>
 struct Pieces {
-    int begin, u, end, tiles, w;
+    PagedSeq sq;                       // lane's tile: its sequence,
+    int b, t, cum;                     // number, place, blocks of one head before it
+    int tiles, begin, u, end, w;
+
+    static __device__ __forceinline__ bool in_lanes(const PagedArgs& a) { return a.batch <= 64 && a.tiles <= 64 && a.first_tile == 0; }
+
+    static __device__ __forceinline__ int sum_before_lane(int v) {
+        const int lane = threadIdx.x & 63;
+        int s = v;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const int o = __shfl_up(s, m, 64);
+            if (lane >= m) s += o;
+        }
+        return s - v;
+    }
 
     // `least`: blocks of a part at least.  False: nothing to do.
-    template <int R, int BU>
     __device__ __forceinline__ bool start(const PagedArgs& a, int least, PagedLine& l) {
+        int blocks;   // of one head
+        if (in_lanes(a)) {
+            const int lane = threadIdx.x & 63;
+            PagedSeq s = paged_seq(a, min(lane, a.batch - 1));
+            if (lane >= a.batch) s.nq = 0;
+            const int n = min((s.nq * a.group + R - 1) / R, a.tiles), before = sum_before_lane(n);
+            tiles = min(__builtin_amdgcn_readlane(before + n, 63), a.tiles);
+            b = 0;
+#pragma unroll
+            for (int m = 32; m; m >>= 1)
+                if (__shfl(before, b + m, 64) <= lane) b += m;
+            t = lane - __shfl(before, b, 64);
+            sq = PagedSeq{__shfl(s.first, b, 64), __shfl(s.nq, b, 64), __shfl(s.nk, b, 64)};
+            const int mine = lane < tiles ? max(key_blocks<R, BU>(a, sq, t * R).n, 1) : 0;
+            cum = sum_before_lane(mine);
+            blocks = __builtin_amdgcn_readlane(cum + mine, 63);
+        } else if (a.parts) {
+            tiles = make_line<R, BU>(a, l);
+            blocks = l.cum[tiles];
+        }
         if (!a.parts) {
             u = 0;
             end = 1;
             return true;
         }
-        tiles = make_line<R, BU>(a, l);
-        const int all = l.cum[tiles] * a.heads_kv, parts = line_parts(a, all, least);
-        if (blockIdx.x == 0) keep_line(a, l, paged_ws<R>(a), tiles, all, parts);
+        const int all = blocks * a.heads_kv, parts = line_parts(a, all, least);
+        if (blockIdx.x == 0) keep(a, l, all, parts);
         w = (int)xcd_remap(blockIdx.x, (uint32_t)parts);
         begin = u = __builtin_amdgcn_readfirstlane(part_begin(all, parts, w));
         end = __builtin_amdgcn_readfirstlane(part_begin(all, parts, w + 1));
         return (int)blockIdx.x < parts;
     }
-    template <int R, int BU>
+
+    // Leaves the line for the join.
+    __device__ __forceinline__ void keep(const PagedArgs& a, const PagedLine& l, int all, int parts) {
+        const PagedWs ws = paged_ws<R>(a);
+        if (threadIdx.x == 0) {
+            ws.head[0] = tiles;
+            ws.head[1] = all;
+            ws.head[2] = parts;
+            ws.cum[tiles] = all / a.heads_kv;
+        }
+        for (int i = threadIdx.x; i < tiles; i += 256) {   // in lanes: i is this lane's tile
+            PagedSeq s = sq;
+            int c = cum, place = t;
+            if (!in_lanes(a)) {
+                const int j = last_at_most(a.batch, [&](int k) { return l.first[k]; }, i);
+                s = paged_seq(a, j);
+                c = l.cum[i];
+                place = i - l.first[j];
+            }
+            ws.cum[i] = c;
+            ws.first[i] = s.first;
+            ws.nq[i] = s.nq;
+            ws.tile[i] = place;
+        }
+    }
+
+    __device__ __forceinline__ void from_lanes(int i, Piece& p) {
+        p.b = __builtin_amdgcn_readlane(b, i);
+        p.t = __builtin_amdgcn_readlane(t, i);
+        p.sq = PagedSeq{__builtin_amdgcn_readlane(sq.first, i), __builtin_amdgcn_readlane(sq.nq, i),
+                        __builtin_amdgcn_readlane(sq.nk, i)};
+    }
+
     __device__ __forceinline__ bool next(const PagedArgs& a, PagedLine& l, Piece& p) {
         if (u >= end) return false;
         if (!a.parts) {
+            const int64_t i = (int64_t)a.first_tile + blockIdx.x / (uint32_t)a.heads_kv;
             p.h = (int)(blockIdx.x % (uint32_t)a.heads_kv);
-            if (!find_tile<R>(a, (int64_t)a.first_tile + blockIdx.x / (uint32_t)a.heads_kv, p.b, p.t, l.part64)) return false;
+            if (in_lanes(a)) {
+                if (i >= tiles) return false;
+                from_lanes((int)i, p);
+            } else {
+                if (!find_tile<R>(a, i, p.b, p.t, l.part64)) return false;
+                p.sq = paged_seq(a, p.b);
+            }
             p.k0 = 0;
-            p.k1 = key_blocks<R, BU>(a, paged_seq(a, p.b), p.t * R).n;
+            p.k1 = key_blocks<R, BU>(a, p.sq, p.t * R).n;
             p.result = -1;
             u = end;
             return true;
         }
         const int heads = a.heads_kv;
-        const int t = __builtin_amdgcn_readfirstlane(last_at_most(tiles, [&](int j) { return l.cum[j] * heads; }, u));
-        const int c = __builtin_amdgcn_readfirstlane(l.cum[t]), n = __builtin_amdgcn_readfirstlane(l.cum[t + 1]) - c;
-        p.b = __builtin_amdgcn_readfirstlane(last_at_most(a.batch, [&](int j) { return l.first[j]; }, t));
-        p.t = t - __builtin_amdgcn_readfirstlane(l.first[p.b]);
+        int c, n;
+        if (in_lanes(a)) {
+            const int lane = threadIdx.x & 63;
+            const int i = __builtin_popcountll(__ballot(lane < tiles && cum * heads <= u)) - 1;
+            from_lanes(i, p);
+            c = __builtin_amdgcn_readlane(cum, i);
+            n = max(key_blocks<R, BU>(a, p.sq, p.t * R).n, 1);
+        } else {
+            const int i = __builtin_amdgcn_readfirstlane(last_at_most(tiles, [&](int j) { return l.cum[j] * heads; }, u));
+            c = __builtin_amdgcn_readfirstlane(l.cum[i]);
+            n = __builtin_amdgcn_readfirstlane(l.cum[i + 1]) - c;
+            p.b = __builtin_amdgcn_readfirstlane(last_at_most(a.batch, [&](int j) { return l.first[j]; }, i));
+            p.t = i - __builtin_amdgcn_readfirstlane(l.first[p.b]);
+            p.sq = paged_seq(a, p.b);
+        }
         p.h = (u - c * heads) / n;
         p.k0 = u - c * heads - p.h * n;
         p.k1 = min(n, p.k0 + end - u);
@@ -313,7 +387,7 @@ __device__ __forceinline__ KeyPlace key_place(const PagedArgs& a, int entry, int
 template <typename T, bool E4>
 __device__ __forceinline__ float value_at(const PagedArgs& a, const int32_t* table, int h, int key, int e) {
     const KeyPlace p = key_place(a, page_entry(a, table, key), key, INT32_MAX);
-    const char* row = (const char*)a.v + (uint64_t)p.v * (E4 ? 8 : 16) + h * a.v_head;
+    const char* row = (const char*)a.v + (uint64_t)p.v * 16 + h * a.v_head;
     if (E4) return decode1(((const uint8_t*)row)[e], scale_value(a.vs[p.s + h * a.s_head]));
     return to_f32(((const T*)row)[e]);
 }

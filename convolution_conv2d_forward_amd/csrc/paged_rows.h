@@ -9,6 +9,8 @@ namespace conv2d {
 
 namespace {
 
+typedef const __attribute__((address_space(1))) uint8_t* GlobalBytes;
+
 // 16 of the rows (new token, head of the group) that share a key head a
 // workgroup, whose four waves take a quarter of a block's keys each: straight
 // from memory into the operands of the matrix cores, the next block's loads in
@@ -36,7 +38,7 @@ struct PagedRows {
     typedef typename std::conditional<E4, typename Codes<T>::type, u32x4>::type VT;
     u32x4 k[NT][KL];
     VT v[NJ][VC];
-    uint32_t scales;   // of this lane's key: K's in the lower half wave, V's in the upper
+    uint8_t scales;    // of this lane's key: K's in the lower half wave, V's in the upper
     uint32_t there;    // keys of the tile that there are
 
     // First element of product step s in lane group g.
@@ -45,43 +47,41 @@ struct PagedRows {
     static __device__ __forceinline__ int k_row(int t, int r) { return sizeof(T) == 2 ? 8 * (r >> 2) + 4 * t + (r & 3) : 16 * t + r; }
     static __device__ __forceinline__ int v_row(int j, int g) { return sizeof(T) == 2 ? 8 * g + j : 16 * (j >> 2) + 4 * g + (j & 3); }
 
-    __device__ __forceinline__ void load(const PagedArgs& a, int entry, int k0, int nk, int h, int lane) {
+    __device__ __forceinline__ void load(const PagedArgs& a, GlobalBytes scale, int entry, int k0, int nk, int h, int lane) {
         int r = lane & 15, g = lane >> 4;
         asm volatile("" : "+v"(r), "+v"(g));   // what follows from them is formed anew for each tile: it would cost registers
         const KeyPlace p = key_place(a, entry, k0 + (lane & (BK - 1)), nk);
         there = (uint32_t)__ballot(p.there) & (BK == 32 ? 0xffffffffu : 0xffffu);
         const char *kb = (const char*)a.k + h * a.k_head, *vb = (const char*)a.v + h * a.v_head;
-        if (E4) scales = (lane < 32 ? a.ks : a.vs)[p.s + h * a.s_head];
+        if (E4) scales = scale[p.s];
+        // Chunks from d on are the row's first instead: no branch stands between
+        // the loads, and step() makes K's zero; V's give outputs that are none.
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const char* row = kb + (uint64_t)from_lane(p.k, k_row(t, r)) * (E4 ? 8 : 16);
+            const char* row = kb + (uint64_t)from_lane(p.k, k_row(t, r)) * 16;
 #pragma unroll
             for (int s = 0; s < KL; ++s) {
                 const int e = element(s * PK, g);
-                k[t][s] = u32x4{0, 0, 0, 0};
-                if constexpr (E4) {
-                    if (e + 16 <= a.d) {
-                        __builtin_memcpy(&k[t][s], row + e, 16);
-                    } else if (e < a.d) {
-                        u32x2 half;
-                        __builtin_memcpy(&half, row + e, 8);
-                        k[t][s] = u32x4{half[0], half[1], 0, 0};
-                    }
-                } else if (e < a.d) {
-                    k[t][s] = *(const u32x4*)(row + e * (int)sizeof(T));
-                }
+                k[t][s] = *(const u32x4*)(row + (e < a.d ? e : 0) * (E4 ? 1 : (int)sizeof(T)));
             }
         }
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            const char* row = vb + (uint64_t)from_lane(p.v, v_row(j, g)) * (E4 ? 8 : 16);
+            const char* row = vb + (uint64_t)from_lane(p.v, v_row(j, g)) * 16;
 #pragma unroll
             for (int c = 0; c < VC; ++c) {
                 const int e = (16 * c + r) * C;
-                v[j][c] = VT{};
-                if (e < a.d) v[j][c] = *(const VT*)(row + e * (E4 ? 1 : (int)sizeof(T)));
+                v[j][c] = *(const VT*)(row + (e < a.d ? e : 0) * (E4 ? 1 : (int)sizeof(T)));
             }
         }
+    }
+
+    __device__ __forceinline__ void cut(int d, int g) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int s = 0; s < KL; ++s)
+                if (element(s * PK, g) >= d) k[t][s] = u32x4{0, 0, 0, 0};
     }
 
     // Operand of K's step t, s.
@@ -107,13 +107,13 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4>::NW), (PagedRows<T, DP, 
     sp.cap = a.softcap;
     sp.scale = a.softcap > 0.0f ? cap_scale(a.scale, a.softcap) : a.scale * kLog2e;
 
-    Pieces pieces;
+    Pieces<16, BU> pieces;
     Piece pc;
-    if (!pieces.start<16, BU>(a, 1, line)) return;
-    while (pieces.next<16, BU>(a, line, pc)) {
+    if (!pieces.start(a, 1, line)) return;
+    while (pieces.next(a, line, pc)) {
         const int b = pc.b, t = pc.t, h = pc.h, first = pc.k0, result = pc.result;
         int last = pc.k1;
-        const PagedSeq sq = paged_seq(a, b);
+        const PagedSeq sq = pc.sq;
         const int32_t* table = a.page_table + (int64_t)b * a.max_pages;
         const KeyBlocks blocks = key_blocks<16, BU>(a, sq, t * 16);
         const int row = t * 16 + r;
@@ -121,8 +121,7 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4>::NW), (PagedRows<T, DP, 
         const int qi = live ? row / a.group : 0, hq = h * a.group + (live ? row - qi * a.group : 0);
         int lo, hi;
         paged_interval(a, sq, qi, live, lo, hi);
-        int w_lo = hi > 0 ? lo : INT32_MAX, w_hi = hi;                     // keys that some row sees, first tokens apart
-        int f_lo = live ? lo : 0, f_hi = live ? hi : INT32_MAX;            // keys that every row sees
+        int f_lo = live ? lo : 0, f_hi = live ? hi : INT32_MAX;   // keys that every row sees, first tokens apart
         u32x4 fq[KS];
         const T* qp = (const T*)a.q + (int64_t)(sq.first + qi) * a.q_s + (int64_t)hq * a.d;
 #pragma unroll
@@ -133,13 +132,9 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4>::NW), (PagedRows<T, DP, 
         }
 #pragma unroll
         for (int m = 1; m < 16; m <<= 1) {
-            w_lo = min(w_lo, __shfl_xor(w_lo, m, 64));
-            w_hi = max(w_hi, __shfl_xor(w_hi, m, 64));
             f_lo = max(f_lo, __shfl_xor(f_lo, m, 64));
             f_hi = min(f_hi, __shfl_xor(f_hi, m, 64));
         }
-        w_lo = __builtin_amdgcn_readfirstlane(w_lo);
-        w_hi = __builtin_amdgcn_readfirstlane(w_hi);
         f_lo = __builtin_amdgcn_readfirstlane(f_lo);
         f_hi = __builtin_amdgcn_readfirstlane(f_hi);
         if (blocks.n == 0) last = first;   // no row sees a key
@@ -149,10 +144,10 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4>::NW), (PagedRows<T, DP, 
         const auto key0 = [&](int i) { return blocks.at(i) * BU + wave * BK; };
         const auto step = [&](R& f, int i) {
             const int k0 = key0(i);
-            if (k0 >= w_hi || (k0 + BK <= w_lo && k0 >= a.sinks)) return;
             const bool whole = k0 + BK <= f_hi && (k0 >= f_lo || k0 + BK <= a.sinks) && f.there == (BK == 32 ? 0xffffffffu : 0xffffu);
             int rr = r, gg = g;
             asm volatile("" : "+v"(rr), "+v"(gg));   // likewise
+            if (a.d < DP) f.cut(a.d, gg);
             f32x4 s[NT] = {};
 #pragma unroll
             for (int u = 0; u < NT; ++u) {
@@ -278,31 +273,51 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4>::NW), (PagedRows<T, DP, 
                 }
             }
         };
-        const auto look = [&](int i) { return i < last ? page_entry(a, table, key0(i) + (lane & (BK - 1))) : 0; };
-        const auto load = [&](R& f, int i, int entry) {
-            if (i < last) f.load(a, entry, key0(i), sq.nk, h, lane);
+        // A page's number is read before the loads of the block ahead of its
+        // own: loads end in order, and waiting for one behind them would be
+        // waiting for them.
+        const auto look = [&](int i) {
+            const int e = page_entry(a, table, key0(min(i, last - 1)) + (lane & (BK - 1)));
+            __builtin_amdgcn_sched_barrier(0);
+            return e;
         };
-        int entry = look(first);
-        if constexpr (R::NBUF == 2) {
-            R f[2];
-            load(f[0], first, entry);
-            entry = look(first + 1);
-            for (int i = first; i < last; i += 2) {
-                load(f[1], i + 1, entry);
-                entry = look(i + 2);
-                step(f[0], i);
-                load(f[0], i + 2, entry);
-                entry = look(i + 3);
-                if (i + 1 < last) step(f[1], i + 1);
-            }
-        } else {
-            for (int i = first; i < last; ++i) {
-                R f;
-                load(f, i, entry);
-                entry = look(i + 1);
-                step(f, i);
+        // Kept as an address: made in the loop, the choice between two arguments
+        // would be a load.
+        uint64_t scale_at = E4 ? (uint64_t)((lane < 32 ? a.ks : a.vs) + h * a.s_head) : 0;
+        asm volatile("" : "+v"(scale_at));
+        const GlobalBytes scale = (GlobalBytes)scale_at;
+        // The last block's loads are made again rather than left out: with a
+        // branch around loads, or out of the loop between them, the compiler
+        // waits for all of them.
+        const auto load = [&](R& f, int i, int entry) {
+            f.load(a, scale, entry, key0(min(i, last - 1)), sq.nk, h, lane);
+        };
+        if (first < last) {
+            int e0 = look(first), e1 = look(first + 1);
+            if constexpr (R::NBUF == 2) {
+                R f[2];
+                load(f[0], first, e0);
+                for (int i = first; i + 1 < last; i += 2) {
+                    e0 = look(i + 2);
+                    load(f[1], i + 1, e1);
+                    step(f[0], i);
+                    e1 = look(i + 3);
+                    load(f[0], i + 2, e0);
+                    step(f[1], i + 1);
+                }
+                if ((last - first) & 1) step(f[0], last - 1);
+            } else {
+                for (int i = first; i < last; ++i) {
+                    R f;
+                    load(f, i, e0);
+                    e0 = e1;
+                    e1 = look(i + 2);
+                    step(f, i);
+                }
             }
         }
+
+        wait_vmem<0>();   // or the next piece's first loads would be counted with the repeated ones
 
         // The waves' results: the maxima and sums first, then the outputs at
         // the common maximum.  Wave w adds up output blocks w, w + NW ...

@@ -58,13 +58,13 @@ __global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_ti
     const float tscale = CAP == kCapTurned ? fminf(fabsf(a.scale) / a.softcap * (2.0f * kLog2e), FLT_MAX)
                          : CAP             ? cap_scale(fabsf(a.scale), a.softcap)
                                            : 0.0f;
-    Pieces pieces;
+    Pieces<R, BK> pieces;
     Piece pc;
-    if (!pieces.start<R, BK>(a, 1, line)) return;
-    while (pieces.next<R, BK>(a, line, pc)) {
+    if (!pieces.start(a, 1, line)) return;
+    while (pieces.next(a, line, pc)) {
         const int h = pc.h, first = pc.k0;
         int last = pc.k1;
-        const PagedSeq sq = paged_seq(a, pc.b);
+        const PagedSeq sq = pc.sq;
         const int32_t* table = a.page_table + (int64_t)pc.b * a.max_pages;
         const KeyBlocks blocks = key_blocks<R, BK>(a, sq, pc.t * R);
         if (blocks.n == 0) last = first;   // no row sees a key
@@ -144,8 +144,8 @@ __global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_ti
                     const int r = r0 + i * (256 / CPR), c = (tid % CPR) ^ C::swizzle(r);
                     const uint32_t pk = from_lane(p.k, r), pv = from_lane(p.v, r);
                     if (c < chunks) {
-                        f.k[i] = *(const typename P::Code*)(kb + (uint64_t)pk * 8 + c * C::C);
-                        f.v[i] = *(const typename P::Code*)(vb + (uint64_t)pv * 8 + c * C::C);
+                        f.k[i] = *(const typename P::Code*)(kb + (uint64_t)pk * 16 + c * C::C);
+                        f.v[i] = *(const typename P::Code*)(vb + (uint64_t)pv * 16 + c * C::C);
                     }
                 }
             }

@@ -112,7 +112,7 @@ typedef struct {
     int64_t v_page_strides[3];
     int64_t scale_strides[3];      /* of both scales; all 0 (default): dense */
     int32_t heads_q, heads_kv;     /* heads_kv divides heads_q; query head h reads key head h / (heads_q / heads_kv) */
-    int32_t head_dim;              /* <= 256; a multiple of 16 bytes of dtype, and of 8 for E4M3 */
+    int32_t head_dim;              /* <= 256; a row of a head in q and in the pages is a multiple of 16 bytes */
     int32_t page_size;             /* 1 .. 2^16 */
     int32_t window;                /* > 0: keys at a distance below `window`; 0 (default): all */
     int32_t sinks;                 /* >= 0, default 0: keys 0 .. sinks - 1 are seen beyond the window too */
@@ -129,8 +129,8 @@ CONV2D_API void paged_attention_params_init(paged_attention_params_t* p);
 /* Errors: INVALID_ARG for a null pointer, a value outside its range or a
  * negative stride; INCOMPATIBLE_SHAPES for heads_kv not dividing heads_q or a
  * token stride below its row; UNSUPPORTED for I8, head_dim beyond 256 or not
- * such a multiple, strides that are not multiples of 16 bytes (E4M3 pages: of
- * 8), and a cache_dtype that is neither dtype nor E4M3. */
+ * such a multiple, strides that are not multiples of 16 bytes (the scales' may
+ * be any), and a cache_dtype that is neither dtype nor E4M3. */
 CONV2D_API conv_status_t paged_attention_desc_create(const paged_attention_params_t* p, paged_attention_desc_t* out);
 CONV2D_API void paged_attention_desc_destroy(paged_attention_desc_t d);
 
@@ -164,12 +164,12 @@ CONV2D_API conv_status_t paged_attention_workspace_bytes(paged_attention_desc_t 
  * values with 16 bits in sequences' tiles of up to 16 rows (new tokens of the
  * call times heads_q / heads_kv per sequence at most so many), rounded to bf16
  * beyond, and a capped score is off as attention_forward's is.
- * Errors: INVALID_ARG for a null or misaligned pointer (16 bytes; E4M3 pages
- * 8), a negative size, tokens or batch beyond 2^30, max_pages * page_size
- * beyond 2^30, or a workspace that is too small; UNSUPPORTED for more than
- * 2^30 rows of a key head, 2^24 workgroups and more, and pages that reach
- * beyond 2^32 units of 16 bytes (E4M3: of 8); ALIAS if out overlaps an input
- * or the workspace, or the workspace an input. */
+ * Errors: INVALID_ARG for a null or misaligned pointer (16 bytes; lengths,
+ * offsets and the table 4), a negative size, tokens or batch beyond 2^30,
+ * max_pages * page_size beyond 2^30, or a workspace that is too small;
+ * UNSUPPORTED for more than 2^30 rows of a key head and pages that reach beyond
+ * 2^36 bytes (their scales: 2^32); ALIAS if out overlaps an input or the
+ * workspace, or the workspace an input. */
 CONV2D_API conv_status_t paged_attention_forward(paged_attention_desc_t d, int64_t tokens, int64_t batch,
                                                  int64_t max_pages, const void* q, const int32_t* q_offsets,
                                                  const int32_t* kv_lens, const int32_t* page_table, int64_t n_pages,

@@ -107,7 +107,9 @@ def test_paged_attention_refusals():
     inv, shapes, uns, alias = m.CONV_ERR_INVALID_ARG, m.CONV_ERR_INCOMPATIBLE_SHAPES, m.CONV_ERR_UNSUPPORTED, m.CONV_ERR_ALIAS
     assert bad(0, 1, 64, 16) == inv and bad(4, 3, 64, 16) == shapes and bad(4, 2, 0, 16) == inv and bad(4, 2, 64, 0) == inv
     assert bad(4, 2, 264, 16) == uns and bad(4, 2, 62, 16) == uns and bad(4, 2, 60, 16, dtype="bf16") == uns
-    assert bad(4, 2, 20, 16, cache_dtype="e4m3") == uns and bad(4, 2, 64, 16, dtype="bf16", cache_dtype="f32") == uns
+    assert bad(4, 2, 20, 16, cache_dtype="e4m3") == uns and bad(4, 2, 72, 16, dtype="bf16", cache_dtype="e4m3") == uns
+    assert bad(4, 2, 64, 16, dtype="bf16", cache_dtype="e4m3", k_page_strides=(2056, 128, 64)) == uns
+    assert bad(4, 2, 64, 16, dtype="bf16", cache_dtype="f32") == uns
     assert bad(4, 2, 64, 16, window=-1) == inv and bad(4, 2, 64, 16, sinks=-1) == inv and bad(4, 2, 64, 16, softcap=-1.0) == inv
     assert bad(4, 2, 64, 16, softcap=math.nan) == inv and bad(4, 2, 64, 16, scale=math.inf) == inv
     assert bad(4, 2, 64, 16, q_stride=255) == shapes and bad(4, 2, 64, 16, q_stride=258) == uns
@@ -124,7 +126,7 @@ def test_paged_attention_refusals():
     assert f(max_pages=1 << 27) == inv and f(tokens=1 << 30) == uns and f(n_pages=1 << 27) == inv
     for name in ("q", "off", "kv", "tab", "kp", "vp", "ks", "vs", "out"):
         assert f(**{name: None}) == inv, name
-    assert f(q=q + 8) == inv and f(kp=kp + 4) == inv and f(off=off + 2) == inv and f(ws=ws + 8) == inv
+    assert f(q=q + 8) == inv and f(kp=kp + 8) == inv and f(off=off + 2) == inv and f(ws=ws + 8) == inv
     assert f(out=q) == alias and f(out=off) == alias and f(out=ks) == alias and f(out=kp + 64) == alias
     assert f(tokens=0, q=None, out=None) == m.CONV_OK and f(batch=0, off=None) == m.CONV_OK
     if need:

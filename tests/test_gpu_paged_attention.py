@@ -66,7 +66,7 @@ def _check(q_lens, kv_lens, hq, hk, d, ps, dtype, cache, seed=0, first=0, extra=
 DIMS = {"bf16": [8, 24, 32, 64, 72, 80, 96, 128, 136, 200, 256], "f32": [4, 20, 32, 64, 96, 100, 128, 160, 256]}
 
 
-@pytest.mark.parametrize("dtype,cache,d", [(t, c, d) for t, c in KINDS for d in DIMS[t] if c == t or d % 8 == 0])
+@pytest.mark.parametrize("dtype,cache,d", [(t, c, d) for t, c in KINDS for d in DIMS[t] if c == t or d % 16 == 0])
 @pytest.mark.parametrize("q_len", [1, 9, 70])
 def test_head_dims(q_len, dtype, cache, d):
     _check([q_len, q_len - 1], [150, 131], 4, 2, d, 16, dtype, cache, seed=d, softcap=30.0)
