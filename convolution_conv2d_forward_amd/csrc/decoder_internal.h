@@ -64,6 +64,7 @@ struct PagedArgs {
     int32_t heads_q, heads_kv, group, d;
     int32_t window, sinks;
     DivU32 page_size;
+    int32_t group_heads, head_groups;   // key heads that a workgroup takes at once, and how many such groups there are
     int32_t tiles;               // row tiles of all sequences, at most
     int32_t first_tile;          // of this launch, where parts == 0
     int32_t parts;               // workgroups that the keys of all tiles are divided among, at most; 0: one a tile and head
@@ -73,6 +74,7 @@ struct PagedArgs {
 // Workgroups and workspace that a call of these sizes runs with.
 struct PagedPlan {
     int32_t rows;                // of a tile: 16, 64 or 128
+    int32_t group_heads;
     int32_t tiles, parts;
     int64_t ws_bytes;
 };

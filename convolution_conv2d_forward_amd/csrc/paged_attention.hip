@@ -9,10 +9,10 @@ namespace conv2d {
 namespace {
 
 // The results of a (tile, head): `n` of them, the first in `slot0` of the
-// workspace, the others in every second one from `slot1` on.
+// workspace, the others `step` slots apart from `slot1` on.
 struct Results {
-    int n, slot0, slot1;
-    __device__ __forceinline__ int slot(int i) const { return i == 0 ? slot0 : slot1 + 2 * i; }
+    int n, slot0, slot1, step;
+    __device__ __forceinline__ int slot(int i) const { return i == 0 ? slot0 : slot1 + step * i; }
 };
 
 // Those of tile t, and where row r of it goes; n = 0 where there is nothing to
@@ -22,14 +22,15 @@ __device__ __forceinline__ Results results_of(const PagedArgs& a, const PagedWs&
     // At once: t is at most the tiles that the line has room for.
     const int tiles = w.head[0], all = w.head[1], parts = w.head[2], c = w.cum[t], end = w.cum[t + 1];
     const int first_row = w.first[t], nq = w.nq[t], place = w.tile[t];
-    Results res{0, 0, 0};
+    Results res{0, 0, 0, 0};
     const int row = place * R + r;
     if (t >= tiles || row >= nq * a.group) return res;
     const int qi = row / a.group, hq = h * a.group + row - qi * a.group, n = end - c;
     out = (T*)a.out + (int64_t)(first_row + qi) * a.o_s + (int64_t)hq * a.d;
-    const int begin = c * a.heads_kv + h * n, first = part_of(all, parts, begin), last = part_of(all, parts, begin + n - 1);
+    const int gh = a.group_heads, hg = h / gh, sub = h - hg * gh;
+    const int begin = c * a.head_groups + hg * n, first = part_of(all, parts, begin), last = part_of(all, parts, begin + n - 1);
     if (first == last) return res;
-    return Results{last - first + 1, 2 * first + (part_begin(all, parts, first) != begin), 2 * first};
+    return Results{last - first + 1, (2 * first + (part_begin(all, parts, first) != begin)) * gh + sub, 2 * first * gh + sub, 2 * gh};
 }
 
 // Few results: as many threads as a row is wide add up its outputs.
@@ -143,7 +144,7 @@ __global__ __launch_bounds__(256) void paged_join_many(PagedArgs a) {
 template <typename T, int R, int DP>
 hipError_t join(const PagedArgs& a, hipStream_t s) {
     const int64_t units = (int64_t)a.tiles * a.heads_kv;
-    if (a.parts >= 8 * units) {
+    if (a.parts >= 8 * (int64_t)a.tiles * a.head_groups) {
         paged_join_many<T, R, DP><<<dim3((uint32_t)(units * R)), dim3(256), 0, s>>>(a);
     } else {
         constexpr int rows = 256 / (DP / 4);
@@ -180,12 +181,19 @@ PagedPlan plan_paged_attention(int32_t dtype, bool e4m3, const PagedArgs& a) {
         const int64_t stage = 2 * keys * bytes;
         per_cu = stage <= 16384 ? 3 : stage <= 32768 ? 2 : 1;
     }
-    const int64_t wgs = cus * per_cu, units = (int64_t)p.tiles * a.heads_kv;
+    // Rows of 128 bytes or less beside each other: two heads at once, so that a
+    // workgroup reads 256 bytes of a token (a token of 32 sequences of up to 8192
+    // keys, 8 heads of 128 E4M3: 89 us by heads, 83 by pairs).
+    const int64_t row = (int64_t)a.d * (e4m3 ? 1 : size);
+    const bool pair = p.rows == 16 && (e4m3 ? bytes / size : bytes) <= 128 && a.heads_kv % 2 == 0 && a.k_head == row && a.v_head == row;
+    p.group_heads = pair ? 2 : 1;
+    if (pair) keys /= 2;
+    const int64_t wgs = cus * per_cu, units = (int64_t)p.tiles * (a.heads_kv / p.group_heads);
     const int64_t blocks = ((int64_t)a.max_pages * a.page_size.d + keys - 1) / keys;
     if (p.tiles <= kPagedTiles && a.batch <= kPagedTiles && blocks > 1 && units < 4 * wgs && units * (blocks + 1) < 0x7fffffff) {
         p.parts = (int32_t)(wgs < units * blocks ? wgs : units * blocks);
         if (p.parts > kMostParts) p.parts = kMostParts;
-        p.ws_bytes = line_bytes(p.tiles) + (int64_t)p.parts * 2 * p.rows * (a.d + 2) * 4;
+        p.ws_bytes = line_bytes(p.tiles) + (int64_t)p.parts * 2 * p.group_heads * p.rows * (a.d + 2) * 4;
     }
     return p;
 }
@@ -216,7 +224,7 @@ hipError_t launch_paged_attention(int32_t dtype, bool e4m3, const PagedPlan& p, 
         return f32 ? join<float>(p, a, s) : join<bf16>(p, a, s);
     }
     // A workgroup a tile and head, as many tiles as a launch's grid holds.
-    const int64_t most = most_workgroups(256) / a.heads_kv;
+    const int64_t most = most_workgroups(256) / a.head_groups;
     for (int64_t t = 0; t < p.tiles; t += most) {
         PagedArgs c = a;
         c.first_tile = (int32_t)t;

@@ -7,7 +7,8 @@
 // key on.  One workgroup takes a (tile, head) whole where there are many; else
 // the blocks of all tiles and heads form one line, tile after tile and head
 // after head, which is cut into equal parts, a workgroup each, whatever the
-// sequences' lengths.  A (tile, head) that a cut divides leaves partial results
+// sequences' lengths.  (A workgroup may take two heads at once: then "head" is a
+// pair of them.)  A (tile, head) that a cut divides leaves partial results
 // in the workspace, two at most a workgroup (one that its part begins with, one
 // that it ends with), which a second launch joins.
 //
@@ -196,8 +197,8 @@ __device__ __forceinline__ int part_of(int all, int parts, int block) {
 
 // The workspace: the line (tiles, blocks of all heads, parts, then for each tile
 // the blocks before it, its sequence's first row and rows of q, and its place
-// among the sequence's tiles), then the parts' outputs, R rows of d for each of
-// two results, then their (running maximum, sum).
+// among the sequence's tiles), then the parts' outputs, R rows of d for each head
+// of each of two results, then their (running maximum, sum).
 struct PagedWs {
     int32_t* head;
     int32_t *cum, *first, *nq, *tile;
@@ -214,16 +215,16 @@ __device__ __forceinline__ PagedWs paged_ws(const PagedArgs& a) {
     w.nq = w.first + a.tiles + 1;
     w.tile = w.nq + a.tiles + 1;
     w.out = (float*)((char*)a.ws + line_bytes(a.tiles));
-    w.stat = (f32x2*)(w.out + (int64_t)a.parts * 2 * R * a.d);
+    w.stat = (f32x2*)(w.out + (int64_t)a.parts * 2 * a.group_heads * R * a.d);
     return w;
 }
 
-// The pieces of a workgroup: blocks k0 .. k1 - 1 of a (tile, head).
+// The pieces of a workgroup: blocks k0 .. k1 - 1 of a (tile, group of heads).
 struct Piece {
     PagedSeq sq;
-    int b, t, h;    // sequence, tile of it, head
+    int b, t, h;    // sequence, tile of it, group of heads
     int k0, k1;
-    int result;     // in the workspace; -1 where the piece is all of its (tile, head)
+    int result;     // in the workspace; -1 where the piece is all of its (tile, group)
 };
 
 // Up to 64 sequences and tiles are kept in the lanes of each wave, a tile a lane:
@@ -275,7 +276,7 @@ struct Pieces {
             end = 1;
             return true;
         }
-        const int all = blocks * a.heads_kv, parts = line_parts(a, all, least);
+        const int all = blocks * a.head_groups, parts = line_parts(a, all, least);
         if (blockIdx.x == 0) keep(a, l, all, parts);
         w = (int)xcd_remap(blockIdx.x, (uint32_t)parts);
         begin = u = __builtin_amdgcn_readfirstlane(part_begin(all, parts, w));
@@ -290,7 +291,7 @@ struct Pieces {
             ws.head[0] = tiles;
             ws.head[1] = all;
             ws.head[2] = parts;
-            ws.cum[tiles] = all / a.heads_kv;
+            ws.cum[tiles] = all / a.head_groups;
         }
         for (int i = threadIdx.x; i < tiles; i += 256) {   // in lanes: i is this lane's tile
             PagedSeq s = sq;
@@ -318,8 +319,8 @@ struct Pieces {
     __device__ __forceinline__ bool next(const PagedArgs& a, PagedLine& l, Piece& p) {
         if (u >= end) return false;
         if (!a.parts) {
-            const int64_t i = (int64_t)a.first_tile + blockIdx.x / (uint32_t)a.heads_kv;
-            p.h = (int)(blockIdx.x % (uint32_t)a.heads_kv);
+            const int64_t i = (int64_t)a.first_tile + blockIdx.x / (uint32_t)a.head_groups;
+            p.h = (int)(blockIdx.x % (uint32_t)a.head_groups);
             if (in_lanes(a)) {
                 if (i >= tiles) return false;
                 from_lanes((int)i, p);
@@ -333,7 +334,7 @@ struct Pieces {
             u = end;
             return true;
         }
-        const int heads = a.heads_kv;
+        const int heads = a.head_groups;
         int c, n;
         if (in_lanes(a)) {
             const int lane = threadIdx.x & 63;

@@ -12,7 +12,8 @@ namespace {
 typedef const __attribute__((address_space(1))) uint8_t* GlobalBytes;
 
 // 16 of the rows (new token, head of the group) that share a key head a
-// workgroup, whose four waves take a quarter of a block's keys each: straight
+// workgroup, whose four waves take a quarter of a block's keys each (or half of
+// them, of one of two heads): straight
 // from memory into the operands of the matrix cores, the next block's loads in
 // flight and the one's after in the page table, no LDS or barrier between.  It
 // is bound by the bytes of keys and values.
@@ -25,7 +26,7 @@ typedef const __attribute__((address_space(1))) uint8_t* GlobalBytes;
 // A lane looks up the page of one key of the wave's tile (the upper half wave
 // the same keys again) and forms its place; the lanes that read a key's row get
 // it by exchange.
-template <typename T, int DP, bool E4>
+template <typename T, int DP, bool E4, int GH>
 struct PagedRows {
     static constexpr int C = Vec<T>::chunk;
     static constexpr int KS = DP * (int)sizeof(T) / 64;               // 64-byte product steps over a row
@@ -34,7 +35,7 @@ struct PagedRows {
     static constexpr int BK = DP * (int)sizeof(T) > 512 ? 16 : 32, NT = BK / 16, NJ = BK / 4;
     static constexpr int OUT = VC * C;                                // 16x16 output blocks
     static constexpr int RB = DP * (int)sizeof(T), NBUF = DP <= 128 ? 2 : 1, OCC = RB <= 256 ? 2 : 1, NW = 4;
-    static constexpr int BU = NW * BK;                                // a block's keys
+    static constexpr int KW = NW / GH, BU = KW * BK;                  // waves of a head; a block's keys
     typedef typename std::conditional<E4, typename Codes<T>::type, u32x4>::type VT;
     u32x4 k[NT][KL];
     VT v[NJ][VC];
@@ -94,10 +95,10 @@ struct PagedRows {
     }
 };
 
-template <typename T, int DP, bool E4>
-__global__ __launch_bounds__((64 * PagedRows<T, DP, E4>::NW), (PagedRows<T, DP, E4>::OCC)) void paged_rows(PagedArgs a) {
-    typedef PagedRows<T, DP, E4> R;
-    constexpr int C = R::C, KS = R::KS, VC = R::VC, NW = R::NW, BK = R::BK, NT = R::NT, NJ = R::NJ, OUT = R::OUT, BU = R::BU;
+template <typename T, int DP, bool E4, int GH>
+__global__ __launch_bounds__((64 * PagedRows<T, DP, E4, GH>::NW), (PagedRows<T, DP, E4, GH>::OCC)) void paged_rows(PagedArgs a) {
+    typedef PagedRows<T, DP, E4, GH> R;
+    constexpr int C = R::C, KS = R::KS, VC = R::VC, NW = R::NW, KW = R::KW, BK = R::BK, NT = R::NT, NJ = R::NJ, OUT = R::OUT, BU = R::BU;
     __shared__ PagedLine line;
     __shared__ f32x2 stat[NW][16];
     __shared__ __align__(16) f32x4 part[NW][OUT][64];
@@ -111,7 +112,8 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4>::NW), (PagedRows<T, DP, 
     Piece pc;
     if (!pieces.start(a, 1, line)) return;
     while (pieces.next(a, line, pc)) {
-        const int b = pc.b, t = pc.t, h = pc.h, first = pc.k0, result = pc.result;
+        const int b = pc.b, t = pc.t, sub = wave % GH, h = pc.h * GH + sub, first = pc.k0;
+        const int64_t result = (int64_t)pc.result * GH + sub;   // below 0: none
         int last = pc.k1;
         const PagedSeq sq = pc.sq;
         const int32_t* table = a.page_table + (int64_t)b * a.max_pages;
@@ -141,7 +143,7 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4>::NW), (PagedRows<T, DP, 
 
         f32x4 o[OUT] = {};
         float m_run = -INFINITY, l_run = 0.0f;
-        const auto key0 = [&](int i) { return blocks.at(i) * BU + wave * BK; };
+        const auto key0 = [&](int i) { return blocks.at(i) * BU + wave / GH * BK; };
         const auto step = [&](R& f, int i) {
             const int k0 = key0(i);
             const bool whole = k0 + BK <= f_hi && (k0 >= f_lo || k0 + BK <= a.sinks) && f.there == (BK == 32 ? 0xffffffffu : 0xffffu);
@@ -319,18 +321,19 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4>::NW), (PagedRows<T, DP, 
 
         wait_vmem<0>();   // or the next piece's first loads would be counted with the repeated ones
 
-        // The waves' results: the maxima and sums first, then the outputs at
-        // the common maximum.  Wave w adds up output blocks w, w + NW ...
+        // The results of a head's waves: the maxima and sums first, then the
+        // outputs at the common maximum.  Its wave w adds up output blocks w,
+        // w + KW ...
         l_run += __shfl_xor(l_run, 16, 64);
         l_run += __shfl_xor(l_run, 32, 64);
         if (g == 0) stat[wave][r] = f32x2{m_run, l_run};
         __syncthreads();
         float top = -INFINITY, total = 0.0f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) top = fmaxf(top, stat[w][r][0]);
+        for (int w = 0; w < KW; ++w) top = fmaxf(top, stat[w * GH + sub][r][0]);
         const float base = top == -INFINITY ? 0.0f : top;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) total += __builtin_amdgcn_exp2f(stat[w][r][0] - base) * stat[w][r][1];
+        for (int w = 0; w < KW; ++w) total += __builtin_amdgcn_exp2f(stat[w * GH + sub][r][0] - base) * stat[w * GH + sub][r][1];
         const float fade = __builtin_amdgcn_exp2f(m_run - base);
 #pragma unroll
         for (int d = 0; d < OUT; ++d) part[wave][d][lane] = o[d] * fade;
@@ -339,7 +342,7 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4>::NW), (PagedRows<T, DP, 
         T* op = (T*)a.out + (int64_t)(sq.first + qi) * a.o_s + (int64_t)hq * a.d;
         const float inv = total == 0.0f ? 0.0f : 1.0f / total;
         // A lane's chunk c of its row i: C consecutive outputs, one of each of C blocks.
-        for (int ci = wave; ci < VC * 4; ci += NW) {
+        for (int ci = wave / GH; ci < VC * 4; ci += KW) {
             const int c = ci >> 2, i = ci & 3, at = (16 * c + 4 * g + i) * C;
             if (at >= a.d) continue;
             float x[C];
@@ -347,28 +350,35 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4>::NW), (PagedRows<T, DP, 
             for (int e = 0; e < C; ++e) {
                 x[e] = 0.0f;
 #pragma unroll
-                for (int w = 0; w < NW; ++w) x[e] += ((const float*)&part[w][c * C + e][lane])[i];
+                for (int w = 0; w < KW; ++w) x[e] += ((const float*)&part[w * GH + sub][c * C + e][lane])[i];
             }
-            if (result < 0) {
+            if (pc.result < 0) {
                 T y[C];
 #pragma unroll
                 for (int e = 0; e < C; ++e) y[e] = from_f32<T>(x[e] * inv);
                 __builtin_memcpy(op + at, y, 16);
             } else {
-                float* wo = paged_ws<16>(a).out + ((int64_t)result * 16 + r) * a.d + at;
+                float* wo = paged_ws<16>(a).out + (result * 16 + r) * a.d + at;
 #pragma unroll
                 for (int e = 0; e < C; ++e) wo[e] = x[e];
             }
         }
-        if (result >= 0 && wave == 0 && g == 0) paged_ws<16>(a).stat[(int64_t)result * 16 + r] = f32x2{top, total};
+        if (pc.result >= 0 && wave < GH && g == 0) paged_ws<16>(a).stat[result * 16 + r] = f32x2{top, total};
     }
+}
+
+template <typename T, int DP, bool E4, int GH>
+hipError_t run(const PagedArgs& a, hipStream_t s) {
+    const uint32_t grid = a.parts ? (uint32_t)a.parts : (uint32_t)a.tiles * (uint32_t)a.head_groups;
+    paged_rows<T, DP, E4, GH><<<dim3(grid), dim3(256), 0, s>>>(a);
+    return hipGetLastError();
 }
 
 template <typename T, int DP, bool E4>
 hipError_t run(const PagedArgs& a, hipStream_t s) {
-    const uint32_t grid = a.parts ? (uint32_t)a.parts : (uint32_t)a.tiles * (uint32_t)a.heads_kv;
-    paged_rows<T, DP, E4><<<dim3(grid), dim3(256), 0, s>>>(a);
-    return hipGetLastError();
+    if constexpr (DP * (E4 ? 1 : (int)sizeof(T)) <= 128)
+        if (a.group_heads == 2) return run<T, DP, E4, 2>(a, s);
+    return run<T, DP, E4, 1>(a, s);
 }
 
 }  // namespace

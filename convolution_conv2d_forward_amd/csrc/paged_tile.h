@@ -398,7 +398,7 @@ __global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_ti
 
 template <typename T, int DP, int KW, bool E4>
 hipError_t run(const PagedArgs& a, hipStream_t s) {
-    const dim3 grid(a.parts ? (uint32_t)a.parts : (uint32_t)a.tiles * (uint32_t)a.heads_kv), block(256);
+    const dim3 grid(a.parts ? (uint32_t)a.parts : (uint32_t)a.tiles * (uint32_t)a.head_groups), block(256);
     if (a.softcap == 0.0f)
         paged_tile<T, DP, KW, kCapNone, E4><<<grid, block, 0, s>>>(a);
     else if (sizeof(T) == 4 || a.softcap > kMostTurned)
