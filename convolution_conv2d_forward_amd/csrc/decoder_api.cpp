@@ -154,6 +154,7 @@ PagedArgs paged_args(const paged_attention_params_t& p, int64_t tokens, int64_t 
     a.heads_q = p.heads_q; a.heads_kv = p.heads_kv; a.group = p.heads_q / p.heads_kv; a.d = p.head_dim;
     a.window = p.window; a.sinks = p.sinks;
     a.page_size = make_divu32((uint32_t)p.page_size);
+    a.group_div = make_divu32((uint32_t)a.group);
     a.scale = p.scale; a.softcap = p.softcap;
     return a;
 }

@@ -63,7 +63,7 @@ struct PagedArgs {
     int32_t tokens, batch, max_pages, n_pages;
     int32_t heads_q, heads_kv, group, d;
     int32_t window, sinks;
-    DivU32 page_size;
+    DivU32 page_size, group_div;
     int32_t group_heads, head_groups;   // key heads that a workgroup takes at once, and how many such groups there are
     int32_t tiles;               // row tiles of all sequences, at most
     int32_t first_tile;          // of this launch, where parts == 0

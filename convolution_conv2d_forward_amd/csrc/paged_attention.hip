@@ -8,54 +8,44 @@ namespace conv2d {
 
 namespace {
 
-// The results of a (tile, head): `n` of them, the first in `slot0` of the
-// workspace, the others `step` slots apart from `slot1` on.
-struct Results {
-    int n, slot0, slot1, step;
-    __device__ __forceinline__ int slot(int i) const { return i == 0 ? slot0 : slot1 + step * i; }
-};
-
-// Those of tile t, and where row r of it goes; n = 0 where there is nothing to
-// join: one result was written whole.
-template <typename T, int R>
-__device__ __forceinline__ Results results_of(const PagedArgs& a, const PagedWs& w, int t, int h, int r, T*& out) {
-    // At once: t is at most the tiles that the line has room for.
-    const int tiles = w.head[0], all = w.head[1], parts = w.head[2], c = w.cum[t], end = w.cum[t + 1];
-    const int first_row = w.first[t], nq = w.nq[t], place = w.tile[t];
-    Results res{0, 0, 0, 0};
-    const int row = place * R + r;
-    if (t >= tiles || row >= nq * a.group) return res;
-    const int qi = row / a.group, hq = h * a.group + row - qi * a.group, n = end - c;
-    out = (T*)a.out + (int64_t)(first_row + qi) * a.o_s + (int64_t)hq * a.d;
-    const int gh = a.group_heads, hg = h / gh, sub = h - hg * gh;
-    const int begin = c * a.head_groups + hg * n, first = part_of(all, parts, begin), last = part_of(all, parts, begin + n - 1);
-    if (first == last) return res;
-    return Results{last - first + 1, (2 * first + (part_begin(all, parts, first) != begin)) * gh + sub, 2 * first * gh + sub, 2 * gh};
+// Where row r of a (tile, head)'s outputs go; false where there is nothing to
+// join: one result was written whole, or there is no such row.
+template <typename T>
+__device__ __forceinline__ bool out_row(const PagedArgs& a, const PagedRecord& rec, int h, int r, T*& out) {
+    if (rec.n == 0 || r >= rec.rows) return false;
+    const int token = token_of(a, r + rec.skip), hq = h * a.group + r + rec.skip - token * a.group;
+    out = (T*)a.out + (int64_t)(rec.first + token) * a.o_s + (int64_t)hq * a.d;
+    return true;
 }
 
-// Few results: as many threads as a row is wide add up its outputs.
+// The row of the workspace that holds the i-th result's row r of a head.
+template <int R>
+__device__ __forceinline__ int64_t result_row(const PagedArgs& a, const PagedRecord& rec, int sub, int i, int r) {
+    return ((int64_t)(i == 0 ? rec.slot0 : rec.slot1 + 2 * i) * a.group_heads + sub) * R + r;
+}
+
+// Few results: as many threads as a row is wide add up its outputs, 256 / W rows
+// a workgroup.
 template <typename T, int R, int DP>
 __global__ __launch_bounds__(256) void paged_join_few(PagedArgs a) {
-    constexpr int W = DP / 4;
-    const uint32_t at = blockIdx.x * (256 / W) + threadIdx.x / W;
-    const int e = (threadIdx.x % W) * 4, r = (int)(at % R), h = (int)(at / R % (uint32_t)a.heads_kv);
-    const int t = (int)(at / R / (uint32_t)a.heads_kv);
+    constexpr int W = DP / 4, ROWS = 256 / W;
+    const int unit = (int)blockIdx.x / (R / ROWS), r = (int)blockIdx.x % (R / ROWS) * ROWS + (int)threadIdx.x / W;
+    const int sub = unit % a.group_heads, e = ((int)threadIdx.x % W) * 4;
     const PagedWs w = paged_ws<R>(a);
-    if (t >= a.tiles || e >= a.d) return;
+    const PagedRecord rec = w.record[unit / a.group_heads];
     T* out;
-    const Results res = results_of<T, R>(a, w, t, h, r, out);
-    if (res.n == 0) return;
+    if (!out_row<T>(a, rec, unit % a.heads_kv, r, out) || e >= a.d) return;
     float top = -INFINITY, l = 0.0f;
     f32x4 sum{0, 0, 0, 0};
-    for (int s0 = 0; s0 < res.n; s0 += 4) {
+    for (int s0 = 0; s0 < rec.n; s0 += 4) {
         f32x2 st[4];
         f32x4 v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t row = (int64_t)res.slot(min(s0 + i, res.n - 1)) * R + r;
+            const int64_t row = result_row<R>(a, rec, sub, min(s0 + i, rec.n - 1), r);
             st[i] = w.stat[row];
             v[i] = *(const f32x4*)(w.out + row * a.d + e);
-            if (s0 + i >= res.n) st[i] = f32x2{-INFINITY, 0.0f};
+            if (s0 + i >= rec.n) st[i] = f32x2{-INFINITY, 0.0f};
         }
         float m = top;
 #pragma unroll
@@ -68,7 +58,7 @@ __global__ __launch_bounds__(256) void paged_join_few(PagedArgs a) {
         for (int i = 0; i < 4; ++i) {
             const float f = __builtin_amdgcn_exp2f(st[i][0] - base);
             l += f * st[i][1];
-            if (s0 + i < res.n) sum += v[i] * f;
+            if (s0 + i < rec.n) sum += v[i] * f;
         }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -77,28 +67,39 @@ __global__ __launch_bounds__(256) void paged_join_few(PagedArgs a) {
 
 // Many: a workgroup a row.  The results' maxima and sums give each one's
 // factor; then groups of threads, each as wide as the row, add up the outputs
-// of every GROUPS-th result, four loads in flight, and meet in LDS.
+// of every GROUPS-th result, four loads in flight, the first ones while the
+// factors are formed, and meet in LDS.
 constexpr int kMostParts = 1024;
 template <typename T, int R, int DP>
 __global__ __launch_bounds__(256) void paged_join_many(PagedArgs a) {
-    constexpr int W = DP / 4, GROUPS = 256 / W;
+    constexpr int W = DP / 4, GROUPS = 256 / W, UN = 4;
     __shared__ float top_w[4], sum_w[4], factor[kMostParts];
     __shared__ __align__(16) f32x4 part[GROUPS][W];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int r = (int)(blockIdx.x % R), h = (int)(blockIdx.x / R % (uint32_t)a.heads_kv);
-    const int t = (int)(blockIdx.x / R / (uint32_t)a.heads_kv);
+    const int unit = (int)blockIdx.x / R, r = (int)blockIdx.x % R, sub = unit % a.group_heads;
     const PagedWs w = paged_ws<R>(a);
+    const PagedRecord rec = w.record[unit / a.group_heads];
     T* out;
-    const Results res = results_of<T, R>(a, w, t, h, r, out);
-    if (res.n == 0) return;
+    if (!out_row<T>(a, rec, unit % a.heads_kv, r, out)) return;
+    const int grp = tid / W, e = (tid % W) * 4, e_in = min(e, a.d - 4);
     f32x2 st[kMostParts / 256];
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kMostParts / 256; ++i) {
         st[i] = f32x2{-INFINITY, 0.0f};
-        if (tid + 256 * i < res.n) st[i] = w.stat[(int64_t)res.slot(tid + 256 * i) * R + r];
-        top = fmaxf(top, st[i][0]);
+        if (tid + 256 * i < rec.n) st[i] = w.stat[result_row<R>(a, rec, sub, tid + 256 * i, r)];
     }
+    f32x4 v[UN];
+    const auto fetch = [&](int s0) {
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            const int64_t row = result_row<R>(a, rec, sub, min(s0 + i * GROUPS, rec.n - 1), r);
+            v[i] = *(const f32x4*)(w.out + row * a.d + e_in);
+        }
+    };
+    fetch(grp);
+#pragma unroll
+    for (int i = 0; i < kMostParts / 256; ++i) top = fmaxf(top, st[i][0]);
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m, 64));
     if (lane == 0) top_w[wave] = top;
@@ -116,21 +117,12 @@ __global__ __launch_bounds__(256) void paged_join_many(PagedArgs a) {
     if (lane == 0) sum_w[wave] = l;
     __syncthreads();
     l = sum_w[0] + sum_w[1] + sum_w[2] + sum_w[3];
-    const int grp = tid / W, e = (tid % W) * 4;
     f32x4 sum{0, 0, 0, 0};
-    for (int s0 = grp; s0 < res.n; s0 += 4 * GROUPS) {
-        f32x4 v[4];
+    for (int s0 = grp; s0 < rec.n; s0 += UN * GROUPS) {
+        if (s0 != grp) fetch(s0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int s = s0 + i * GROUPS;
-            v[i] = f32x4{0, 0, 0, 0};
-            if (s < res.n && e < a.d) v[i] = *(const f32x4*)(w.out + ((int64_t)res.slot(s) * R + r) * a.d + e);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int s = s0 + i * GROUPS;
-            if (s < res.n) sum += v[i] * factor[s];
-        }
+        for (int i = 0; i < UN; ++i)
+            if (s0 + i * GROUPS < rec.n) sum += v[i] * factor[s0 + i * GROUPS];
     }
     part[grp][tid % W] = sum;
     __syncthreads();
@@ -144,12 +136,10 @@ __global__ __launch_bounds__(256) void paged_join_many(PagedArgs a) {
 template <typename T, int R, int DP>
 hipError_t join(const PagedArgs& a, hipStream_t s) {
     const int64_t units = (int64_t)a.tiles * a.heads_kv;
-    if (a.parts >= 8 * (int64_t)a.tiles * a.head_groups) {
+    if (a.parts >= 8 * (int64_t)a.tiles * a.head_groups)
         paged_join_many<T, R, DP><<<dim3((uint32_t)(units * R)), dim3(256), 0, s>>>(a);
-    } else {
-        constexpr int rows = 256 / (DP / 4);
-        paged_join_few<T, R, DP><<<dim3((uint32_t)((units * R + rows - 1) / rows)), dim3(256), 0, s>>>(a);
-    }
+    else
+        paged_join_few<T, R, DP><<<dim3((uint32_t)(units * (R / (256 / (DP / 4))))), dim3(256), 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -193,7 +183,7 @@ PagedPlan plan_paged_attention(int32_t dtype, bool e4m3, const PagedArgs& a) {
     if (p.tiles <= kPagedTiles && a.batch <= kPagedTiles && blocks > 1 && units < 4 * wgs && units * (blocks + 1) < 0x7fffffff) {
         p.parts = (int32_t)(wgs < units * blocks ? wgs : units * blocks);
         if (p.parts > kMostParts) p.parts = kMostParts;
-        p.ws_bytes = line_bytes(p.tiles) + (int64_t)p.parts * 2 * p.group_heads * p.rows * (a.d + 2) * 4;
+        p.ws_bytes = record_bytes(p.tiles, a.heads_kv / p.group_heads) + (int64_t)p.parts * 2 * p.group_heads * p.rows * (a.d + 2) * 4;
     }
     return p;
 }

@@ -12,9 +12,9 @@
 // in the workspace, two at most a workgroup (one that its part begins with, one
 // that it ends with), which a second launch joins.
 //
-// Lengths and offsets come from the device, so both launches work the line out
-// for themselves: the tiles' blocks are summed up by each workgroup of the
-// first, and left in the workspace for the second.
+// Lengths and offsets come from the device, so each workgroup of the first launch
+// works the line out for itself; together they leave the second one a record of
+// each (tile, head).
 #pragma once
 
 #include "attention_common.h"
@@ -38,6 +38,19 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int b) {
     return s;
 }
 
+// The kernel's argument, read anew: what is formed from it is formed where it
+// is needed.  Otherwise the compiler forms it once, before the first piece, and
+// keeps more in scalar registers than there are.  (With one read, 128-row tiles
+// of bfloat16 have 190 lane reads for a block of 32 matrix instructions.)
+__device__ __forceinline__ const PagedArgs& kernel_args() {
+    auto p = __builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const PagedArgs*)p;
+}
+
+// The new token of a row.
+__device__ __forceinline__ int token_of(const PagedArgs& a, int row) { return (int)divu((uint32_t)row, a.group_div); }
+
 // Blocks of BU keys that rows r0 .. r0 + R - 1 of a sequence see.
 struct KeyBlocks {
     int ns, w0, n;   // ns from the first key on, then n - ns from block w0 on
@@ -45,7 +58,7 @@ struct KeyBlocks {
 };
 template <int R, int BU>
 __device__ __forceinline__ KeyBlocks key_blocks(const PagedArgs& a, PagedSeq s, int r0) {
-    const int p0 = s.nk - s.nq + r0 / a.group, p1 = s.nk - s.nq + (min(r0 + R, s.nq * a.group) - 1) / a.group;
+    const int p0 = s.nk - s.nq + token_of(a, r0), p1 = s.nk - s.nq + token_of(a, min(r0 + R, s.nq * a.group) - 1);
     const int hi = min(p1 + 1, s.nk), lo = a.window && p0 >= a.window ? p0 - a.window + 1 : 0;
     KeyBlocks k{0, 0, 0};
     if (hi <= 0) return k;
@@ -195,26 +208,28 @@ __device__ __forceinline__ int part_of(int all, int parts, int block) {
     return (int)((((int64_t)block + 1) * parts - 1) / all);
 }
 
-// The workspace: the line (tiles, blocks of all heads, parts, then for each tile
-// the blocks before it, its sequence's first row and rows of q, and its place
-// among the sequence's tiles), then the parts' outputs, R rows of d for each head
-// of each of two results, then their (running maximum, sum).
+// The workspace: a record of each (tile, head), then the parts' outputs, R rows
+// of d for each head of each of two results, then their (running maximum, sum).
+struct PagedRecord {
+    int32_t n;             // results to be joined; 0: none
+    int32_t slot0, slot1;  // the first one's, from which the others' are, `step` apart
+    int32_t first, rows;   // the tile's first row of q and, of the sequence's rows from it on, those that there are
+    int32_t skip;          // rows of the first token that belong to the tile before
+    int32_t unused[2];
+};
 struct PagedWs {
-    int32_t* head;
-    int32_t *cum, *first, *nq, *tile;
+    PagedRecord* record;
     float* out;
     f32x2* stat;
 };
-__host__ __device__ __forceinline__ int64_t line_bytes(int tiles) { return (int64_t)(4 + 4 * (tiles + 1)) * 4 / 16 * 16 + 16; }
+__host__ __device__ __forceinline__ int64_t record_bytes(int64_t tiles, int head_groups) {
+    return tiles * head_groups * (int64_t)sizeof(PagedRecord);
+}
 template <int R>
 __device__ __forceinline__ PagedWs paged_ws(const PagedArgs& a) {
     PagedWs w;
-    w.head = (int32_t*)a.ws;
-    w.cum = w.head + 4;
-    w.first = w.cum + a.tiles + 1;
-    w.nq = w.first + a.tiles + 1;
-    w.tile = w.nq + a.tiles + 1;
-    w.out = (float*)((char*)a.ws + line_bytes(a.tiles));
+    w.record = (PagedRecord*)a.ws;
+    w.out = (float*)((char*)a.ws + record_bytes(a.tiles, a.head_groups));
     w.stat = (f32x2*)(w.out + (int64_t)a.parts * 2 * a.group_heads * R * a.d);
     return w;
 }
@@ -234,7 +249,7 @@ template <int R, int BU>
 struct Pieces {
     PagedSeq sq;                       // lane's tile: its sequence,
     int b, t, cum;                     // number, place, blocks of one head before it
-    int tiles, begin, u, end, w;
+    int tiles, begin, end, w;
 
     static __device__ __forceinline__ bool in_lanes(const PagedArgs& a) { return a.batch <= 64 && a.tiles <= 64 && a.first_tile == 0; }
 
@@ -272,41 +287,52 @@ struct Pieces {
             blocks = l.cum[tiles];
         }
         if (!a.parts) {
-            u = 0;
+            begin = 0;
             end = 1;
             return true;
         }
         const int all = blocks * a.head_groups, parts = line_parts(a, all, least);
-        if (blockIdx.x == 0) keep(a, l, all, parts);
+        keep(a, l, all, parts);
         w = (int)xcd_remap(blockIdx.x, (uint32_t)parts);
-        begin = u = __builtin_amdgcn_readfirstlane(part_begin(all, parts, w));
+        begin = __builtin_amdgcn_readfirstlane(part_begin(all, parts, w));
         end = __builtin_amdgcn_readfirstlane(part_begin(all, parts, w + 1));
         return (int)blockIdx.x < parts;
     }
 
-    // Leaves the line for the join.
+    // Leaves records for the join: those of every gridDim.x-th (tile, head), a
+    // thread each.
     __device__ __forceinline__ void keep(const PagedArgs& a, const PagedLine& l, int all, int parts) {
-        const PagedWs ws = paged_ws<R>(a);
-        if (threadIdx.x == 0) {
-            ws.head[0] = tiles;
-            ws.head[1] = all;
-            ws.head[2] = parts;
-            ws.cum[tiles] = all / a.head_groups;
+        const int j = (int)(blockIdx.x + threadIdx.x * gridDim.x), units = a.tiles * a.head_groups;
+        const int i = j / a.head_groups, h = j - i * a.head_groups;
+        if (threadIdx.x >= 64) return;
+        PagedSeq s;
+        int c = 0, place = 0;
+        if (in_lanes(a)) {
+            const int from = min(i, 63);
+            s = PagedSeq{__shfl(sq.first, from, 64), __shfl(sq.nq, from, 64), __shfl(sq.nk, from, 64)};
+            c = __shfl(cum, from, 64);
+            place = __shfl(t, from, 64);
+        } else if (i < tiles) {
+            const int k = last_at_most(a.batch, [&](int m) { return l.first[m]; }, i);
+            s = paged_seq(a, k);
+            c = l.cum[i];
+            place = i - l.first[k];
         }
-        for (int i = threadIdx.x; i < tiles; i += 256) {   // in lanes: i is this lane's tile
-            PagedSeq s = sq;
-            int c = cum, place = t;
-            if (!in_lanes(a)) {
-                const int j = last_at_most(a.batch, [&](int k) { return l.first[k]; }, i);
-                s = paged_seq(a, j);
-                c = l.cum[i];
-                place = i - l.first[j];
+        if (j >= units) return;
+        PagedRecord r{};
+        if (i < tiles) {
+            const int n = max(key_blocks<R, BU>(a, s, place * R).n, 1), from = c * a.head_groups + h * n;
+            const int p0 = part_of(all, parts, from), p1 = part_of(all, parts, from + n - 1), token = token_of(a, place * R);
+            if (p1 > p0) {
+                r.n = p1 - p0 + 1;
+                r.slot0 = 2 * p0 + (part_begin(all, parts, p0) != from);
+                r.slot1 = 2 * p0;
+                r.first = s.first + token;
+                r.skip = place * R - token * a.group;
+                r.rows = s.nq * a.group - place * R;
             }
-            ws.cum[i] = c;
-            ws.first[i] = s.first;
-            ws.nq[i] = s.nq;
-            ws.tile[i] = place;
         }
+        paged_ws<R>(a).record[j] = r;
     }
 
     __device__ __forceinline__ void from_lanes(int i, Piece& p) {
@@ -316,7 +342,8 @@ struct Pieces {
                         __builtin_amdgcn_readlane(sq.nk, i)};
     }
 
-    __device__ __forceinline__ bool next(const PagedArgs& a, PagedLine& l, Piece& p) {
+    // The piece at `u` (begin at first), and where the next one is.
+    __device__ __forceinline__ bool next(const PagedArgs& a, PagedLine& l, int& u, Piece& p) {
         if (u >= end) return false;
         if (!a.parts) {
             const int64_t i = (int64_t)a.first_tile + blockIdx.x / (uint32_t)a.head_groups;

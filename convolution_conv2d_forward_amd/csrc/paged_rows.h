@@ -96,7 +96,8 @@ struct PagedRows {
 };
 
 template <typename T, int DP, bool E4, int GH>
-__global__ __launch_bounds__((64 * PagedRows<T, DP, E4, GH>::NW), (PagedRows<T, DP, E4, GH>::OCC)) void paged_rows(PagedArgs a) {
+__global__ __launch_bounds__((64 * PagedRows<T, DP, E4, GH>::NW), (PagedRows<T, DP, E4, GH>::OCC)) void paged_rows(PagedArgs) {
+    const PagedArgs& a = kernel_args();
     typedef PagedRows<T, DP, E4, GH> R;
     constexpr int C = R::C, KS = R::KS, VC = R::VC, NW = R::NW, KW = R::KW, BK = R::BK, NT = R::NT, NJ = R::NJ, OUT = R::OUT, BU = R::BU;
     __shared__ PagedLine line;
@@ -111,7 +112,9 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4, GH>::NW), (PagedRows<T, 
     Pieces<16, BU> pieces;
     Piece pc;
     if (!pieces.start(a, 1, line)) return;
-    while (pieces.next(a, line, pc)) {
+    int u = pieces.begin;
+    while (pieces.next(kernel_args(), line, u, pc)) {
+        const PagedArgs& a = kernel_args();
         const int b = pc.b, t = pc.t, sub = wave % GH, h = pc.h * GH + sub, first = pc.k0;
         const int64_t result = (int64_t)pc.result * GH + sub;   // below 0: none
         int last = pc.k1;
@@ -120,7 +123,7 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4, GH>::NW), (PagedRows<T, 
         const KeyBlocks blocks = key_blocks<16, BU>(a, sq, t * 16);
         const int row = t * 16 + r;
         const bool live = row < sq.nq * a.group;
-        const int qi = live ? row / a.group : 0, hq = h * a.group + (live ? row - qi * a.group : 0);
+        const int qi = live ? token_of(a, row) : 0, hq = h * a.group + (live ? row - qi * a.group : 0);
         int lo, hi;
         paged_interval(a, sq, qi, live, lo, hi);
         int f_lo = live ? lo : 0, f_hi = live ? hi : INT32_MAX;   // keys that every row sees, first tokens apart
@@ -152,11 +155,11 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4, GH>::NW), (PagedRows<T, 
             if (a.d < DP) f.cut(a.d, gg);
             f32x4 s[NT] = {};
 #pragma unroll
-            for (int u = 0; u < NT; ++u) {
+            for (int t = 0; t < NT; ++t) {
                 float scale = 1.0f;
-                if (E4) scale = scale_value(from_lane(f.scales, R::k_row(u, rr)));
+                if (E4) scale = scale_value(from_lane(f.scales, R::k_row(t, rr)));
 #pragma unroll
-                for (int j = 0; j < KS; ++j) s[u] = mfma_step<T>(f.key(u, j, scale), fq[j], s[u]);
+                for (int j = 0; j < KS; ++j) s[t] = mfma_step<T>(f.key(t, j, scale), fq[j], s[t]);
             }
             u32x4 decoded[E4 ? NJ : 1][E4 ? VC : 1];
             if constexpr (E4) {
@@ -195,12 +198,12 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4, GH>::NW), (PagedRows<T, 
             for (int j = 0; j < 4 * NT; ++j) sc[j] = s[j >> 2][j & 3];
             scores<T>(sp, sc);
 #pragma unroll
-            for (int u = 0; u < NT; ++u)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float x = sc[4 * u + j];
-                    if (!whole) x = sees(k0 + (sizeof(T) == 2 ? 8 * gg + 4 * u + j : 16 * u + 4 * gg + j)) ? x : -INFINITY;
-                    s[u][j] = x;
+                    float x = sc[4 * t + j];
+                    if (!whole) x = sees(k0 + (sizeof(T) == 2 ? 8 * gg + 4 * t + j : 16 * t + 4 * gg + j)) ? x : -INFINITY;
+                    s[t][j] = x;
                     top = fmaxf(top, x);
                 }
             top = fmaxf(top, __shfl_xor(top, 16, 64));
@@ -210,11 +213,11 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4, GH>::NW), (PagedRows<T, 
             m_run = m_new;
             l_run *= fade;
 #pragma unroll
-            for (int u = 0; u < NT; ++u)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    p[u][j] = __builtin_amdgcn_exp2f(s[u][j] - base);
-                    l_run += p[u][j];
+                    p[t][j] = __builtin_amdgcn_exp2f(s[t][j] - base);
+                    l_run += p[t][j];
                 }
 #pragma unroll
             for (int d = 0; d < OUT; ++d) o[d] *= fade;
@@ -339,12 +342,13 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4, GH>::NW), (PagedRows<T, 
         for (int d = 0; d < OUT; ++d) part[wave][d][lane] = o[d] * fade;
         __syncthreads();
         if (!live) continue;
-        T* op = (T*)a.out + (int64_t)(sq.first + qi) * a.o_s + (int64_t)hq * a.d;
+        const PagedArgs& end = kernel_args();
+        T* op = (T*)end.out + (int64_t)(sq.first + qi) * end.o_s + (int64_t)hq * end.d;
         const float inv = total == 0.0f ? 0.0f : 1.0f / total;
         // A lane's chunk c of its row i: C consecutive outputs, one of each of C blocks.
         for (int ci = wave / GH; ci < VC * 4; ci += KW) {
             const int c = ci >> 2, i = ci & 3, at = (16 * c + 4 * g + i) * C;
-            if (at >= a.d) continue;
+            if (at >= end.d) continue;
             float x[C];
 #pragma unroll
             for (int e = 0; e < C; ++e) {
@@ -358,12 +362,12 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4, GH>::NW), (PagedRows<T, 
                 for (int e = 0; e < C; ++e) y[e] = from_f32<T>(x[e] * inv);
                 __builtin_memcpy(op + at, y, 16);
             } else {
-                float* wo = paged_ws<16>(a).out + (result * 16 + r) * a.d + at;
+                float* wo = paged_ws<16>(end).out + (result * 16 + r) * end.d + at;
 #pragma unroll
                 for (int e = 0; e < C; ++e) wo[e] = x[e];
             }
         }
-        if (pc.result >= 0 && wave < GH && g == 0) paged_ws<16>(a).stat[result * 16 + r] = f32x2{top, total};
+        if (pc.result >= 0 && wave < GH && g == 0) paged_ws<16>(end).stat[result * 16 + r] = f32x2{top, total};
     }
 }
 

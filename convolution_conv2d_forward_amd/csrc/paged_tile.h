@@ -33,7 +33,8 @@ struct PagedTile : TileAttn<T, DP, KW> {
 };
 
 template <typename T, int DP, int KW, int CAP, bool E4>
-__global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_tile(PagedArgs a) {
+__global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_tile(PagedArgs) {
+    const PagedArgs& a = kernel_args();
     typedef PagedTile<T, DP, KW, E4> P;
     typedef TileAttn<T, DP, KW> C;
     constexpr bool HALF = C::HALF;
@@ -48,7 +49,6 @@ __global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_ti
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 31, g = lane >> 5, kpart = wave / C::RG;
-    const int chunks = a.d / C::C;
     const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
     // A negative scale goes into Q's signs, and one of zero makes Q zero: a
     // masked score, -inf, is multiplied by the scale later (PLAIN).
@@ -61,7 +61,10 @@ __global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_ti
     Pieces<R, BK> pieces;
     Piece pc;
     if (!pieces.start(a, 1, line)) return;
-    while (pieces.next(a, line, pc)) {
+    int u = pieces.begin;
+    while (pieces.next(kernel_args(), line, u, pc)) {
+        const PagedArgs& a = kernel_args();
+        const int chunks = a.d / C::C;
         const int h = pc.h, first = pc.k0;
         int last = pc.k1;
         const PagedSeq sq = pc.sq;
@@ -74,12 +77,12 @@ __global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_ti
         // (first tokens apart), and those that all of the workgroup see.
         const int row = pc.t * R + wave % C::RG * 32 + n;
         const bool live = row < rows;
-        const int qi = live ? row / a.group : 0, hq = h * a.group + (live ? row - qi * a.group : 0);
+        const int qi = live ? token_of(a, row) : 0, hq = h * a.group + (live ? row - qi * a.group : 0);
         int lo, hi, w_lo, w_hi, f_lo, f_hi, all_lo, all_hi, unused;
         paged_interval(a, sq, qi, live, lo, hi);
         {
             const int r0 = pc.t * R, rw = r0 + wave % C::RG * 32;
-            const auto token = [&](int r) { return __builtin_amdgcn_readfirstlane(min(r, rows - 1) / a.group); };
+            const auto token = [&](int r) { return __builtin_amdgcn_readfirstlane(token_of(a, min(r, rows - 1))); };
             paged_interval(a, sq, token(rw), rw < rows, w_lo, f_hi);
             paged_interval(a, sq, token(rw + 31), rw < rows, f_lo, w_hi);
             paged_interval(a, sq, token(r0), true, unused, all_hi);
@@ -376,21 +379,22 @@ __global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_ti
                 }
         }
         if (!live) continue;
+        const PagedArgs& end = kernel_args();
         const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
-        T* op = (T*)a.out + (int64_t)(sq.first + qi) * a.o_s + (int64_t)hq * a.d;
+        T* op = (T*)end.out + (int64_t)(sq.first + qi) * end.o_s + (int64_t)hq * end.d;
         const int64_t wr = (int64_t)pc.result * R + row - pc.t * R;
-        const PagedWs ws = paged_ws<R>(a);
+        const PagedWs ws = paged_ws<R>(end);
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int e = 32 * d + 8 * q + 4 * g;
                 const f32x4 v{o[d][4 * q], o[d][4 * q + 1], o[d][4 * q + 2], o[d][4 * q + 3]};
-                if (e >= a.d) continue;
+                if (e >= end.d) continue;
                 if (pc.result < 0)
                     *(typename Vec<T>::v4*)(op + e) = from_f32<T>(v * inv);
                 else
-                    *(f32x4*)(ws.out + wr * a.d + e) = v;
+                    *(f32x4*)(ws.out + wr * end.d + e) = v;
             }
         if (pc.result >= 0 && g == 0) ws.stat[wr] = f32x2{m_run, l_run};
     }
