@@ -14,7 +14,7 @@
 //
 // Lengths and offsets come from the device, so each workgroup of the first launch
 // works the line out for itself; together they leave the second one a record of
-// each (tile, head).
+// each (tile, group of heads).
 #pragma once
 
 #include "attention_common.h"
@@ -208,11 +208,11 @@ __device__ __forceinline__ int part_of(int all, int parts, int block) {
     return (int)((((int64_t)block + 1) * parts - 1) / all);
 }
 
-// The workspace: a record of each (tile, head), then the parts' outputs, R rows
+// The workspace: a record of each (tile, group of heads), then the parts' outputs, R rows
 // of d for each head of each of two results, then their (running maximum, sum).
 struct PagedRecord {
     int32_t n;             // results to be joined; 0: none
-    int32_t slot0, slot1;  // the first one's, from which the others' are, `step` apart
+    int32_t slot0, slot1;  // the first one is at slot0, the i-th other at slot1 + 2 i
     int32_t first, rows;   // the tile's first row of q and, of the sequence's rows from it on, those that there are
     int32_t skip;          // rows of the first token that belong to the tile before
     int32_t unused[2];

@@ -145,7 +145,8 @@ CONV2D_API void qk_rope_desc_destroy(qk_rope_desc_t d);
  * slot outside [0, cache_rows) stores neither (a padding token); two tokens
  * must not share a slot.  v null: values are not stored.  attention_forward
  * reads a sequence's keys at one stride, so for it token i of sequence b goes to
- * a row first[b] + i (or first[b] + c i), not to rows of scattered pages.
+ * a row first[b] + i (or first[b] + c i); rows of scattered pages are
+ * paged_attention_forward's (decoder.h).
  * cache_rows is the number of rows of k and v (>= tokens where slots is null).
  * q may be qkv itself with q_stride == qkv_stride (in place); any other
  * overlap of an output with an input or another output returns ALIAS.
