@@ -178,9 +178,13 @@ PagedPlan plan_paged_attention(int32_t dtype, bool e4m3, const PagedArgs& a) {
     const bool pair = p.rows == 16 && (e4m3 ? bytes / size : bytes) <= 128 && a.heads_kv % 2 == 0 && a.k_head == row && a.v_head == row;
     p.group_heads = pair ? 2 : 1;
     if (pair) keys /= 2;
+    // Fewer (tile, group)s than two rounds of workgroups are divided.  (A prompt
+    // of 8192 tokens, two rounds of them: 364 us divided, 316 whole; one of 4096,
+    // one round: 114 and 141.  A token of 128 sequences of up to 2048 keys, two
+    // rounds: 149 and 143; of 192, one and a half: 122 and 135.)
     const int64_t wgs = cus * per_cu, units = (int64_t)p.tiles * (a.heads_kv / p.group_heads);
     const int64_t blocks = ((int64_t)a.max_pages * a.page_size.d + keys - 1) / keys;
-    if (p.tiles <= kPagedTiles && a.batch <= kPagedTiles && blocks > 1 && units < 4 * wgs && units * (blocks + 1) < 0x7fffffff) {
+    if (p.tiles <= kPagedTiles && a.batch <= kPagedTiles && blocks > 1 && units < 2 * wgs && units * (blocks + 8) < 0x7fffffff) {
         p.parts = (int32_t)(wgs < units * blocks ? wgs : units * blocks);
         if (p.parts > kMostParts) p.parts = kMostParts;
         p.ws_bytes = record_bytes(p.tiles, a.heads_kv / p.group_heads) + (int64_t)p.parts * 2 * p.group_heads * p.rows * (a.d + 2) * 4;

@@ -125,7 +125,7 @@ __device__ __forceinline__ int last_at_most(int n, F t, int x) {
 // Fills the line; returns the number of tiles.  A tile without keys counts a
 // block: its rows are zeros that someone has to write.  Offsets that do not
 // ascend may make more tiles than the host has counted: those are left out.
-template <int R, int BU>
+template <int R, int BU, int COST>
 __device__ __forceinline__ int make_line(const PagedArgs& a, PagedLine& l) {
     const int tid = threadIdx.x;
     int n[4], sum = 0, all;
@@ -149,7 +149,7 @@ __device__ __forceinline__ int make_line(const PagedArgs& a, PagedLine& l) {
         n[i] = 0;
         if (t < tiles) {
             const int b = last_at_most(a.batch, [&](int j) { return l.first[j]; }, t);
-            n[i] = max(key_blocks<R, BU>(a, paged_seq(a, b), (t - l.first[b]) * R).n, 1);
+            n[i] = max(key_blocks<R, BU>(a, paged_seq(a, b), (t - l.first[b]) * R).n, 1) + COST;
         }
         sum += n[i];
     }
@@ -242,10 +242,15 @@ struct Piece {
     int result;     // in the workspace; -1 where the piece is all of its (tile, group)
 };
 
+// A (tile, group) counts COST blocks more than it has: what it costs a workgroup
+// to begin another one.  (128-row tiles, chunks of prompts and single tokens:
+// 58.2 us with 0, 55.5 with 2, 55.9 with 3.  Where the workgroups share all of
+// the memory's bandwidth, as with single tokens, 0 is best.)
+//
 // Up to 64 sequences and tiles are kept in the lanes of each wave, a tile a lane:
 // no LDS, no barrier, each length and offset read once (a call of a token of 32
 // sequences: 3 us less than by way of LDS).
-template <int R, int BU>
+template <int R, int BU, int COST>
 struct Pieces {
     PagedSeq sq;                       // lane's tile: its sequence,
     int b, t, cum;                     // number, place, blocks of one head before it
@@ -279,11 +284,11 @@ struct Pieces {
                 if (__shfl(before, b + m, 64) <= lane) b += m;
             t = lane - __shfl(before, b, 64);
             sq = PagedSeq{__shfl(s.first, b, 64), __shfl(s.nq, b, 64), __shfl(s.nk, b, 64)};
-            const int mine = lane < tiles ? max(key_blocks<R, BU>(a, sq, t * R).n, 1) : 0;
+            const int mine = lane < tiles ? max(key_blocks<R, BU>(a, sq, t * R).n, 1) + COST : 0;
             cum = sum_before_lane(mine);
             blocks = __builtin_amdgcn_readlane(cum + mine, 63);
         } else if (a.parts) {
-            tiles = make_line<R, BU>(a, l);
+            tiles = make_line<R, BU, COST>(a, l);
             blocks = l.cum[tiles];
         }
         if (!a.parts) {
@@ -321,11 +326,12 @@ struct Pieces {
         if (j >= units) return;
         PagedRecord r{};
         if (i < tiles) {
-            const int n = max(key_blocks<R, BU>(a, s, place * R).n, 1), from = c * a.head_groups + h * n;
-            const int p0 = part_of(all, parts, from), p1 = part_of(all, parts, from + n - 1), token = token_of(a, place * R);
+            const int n = max(key_blocks<R, BU>(a, s, place * R).n, 1), from = c * a.head_groups + h * (n + COST);
+            const int p0 = part_of(all, parts, from + COST), p1 = part_of(all, parts, from + COST + n - 1);
+            const int token = token_of(a, place * R);
             if (p1 > p0) {
                 r.n = p1 - p0 + 1;
-                r.slot0 = 2 * p0 + (part_begin(all, parts, p0) != from);
+                r.slot0 = 2 * p0 + (part_begin(all, parts, p0) < from);
                 r.slot1 = 2 * p0;
                 r.first = s.first + token;
                 r.skip = place * R - token * a.group;
@@ -346,7 +352,8 @@ struct Pieces {
     __device__ __forceinline__ bool next(const PagedArgs& a, PagedLine& l, int& u, Piece& p) {
         if (u >= end) return false;
         if (!a.parts) {
-            const int64_t i = (int64_t)a.first_tile + blockIdx.x / (uint32_t)a.head_groups;
+            // The last tiles first: they see the most keys.
+            const int64_t i = (int64_t)a.first_tile + (gridDim.x - 1 - blockIdx.x) / (uint32_t)a.head_groups;
             p.h = (int)(blockIdx.x % (uint32_t)a.head_groups);
             if (in_lanes(a)) {
                 if (i >= tiles) return false;
@@ -372,17 +379,18 @@ struct Pieces {
         } else {
             const int i = __builtin_amdgcn_readfirstlane(last_at_most(tiles, [&](int j) { return l.cum[j] * heads; }, u));
             c = __builtin_amdgcn_readfirstlane(l.cum[i]);
-            n = __builtin_amdgcn_readfirstlane(l.cum[i + 1]) - c;
+            n = __builtin_amdgcn_readfirstlane(l.cum[i + 1]) - c - COST;
             p.b = __builtin_amdgcn_readfirstlane(last_at_most(a.batch, [&](int j) { return l.first[j]; }, i));
             p.t = i - __builtin_amdgcn_readfirstlane(l.first[p.b]);
             p.sq = paged_seq(a, p.b);
         }
-        p.h = (u - c * heads) / n;
-        p.k0 = u - c * heads - p.h * n;
-        p.k1 = min(n, p.k0 + end - u);
+        p.h = (u - c * heads) / (n + COST);
+        const int at = u - c * heads - p.h * (n + COST), size = min(n + COST - at, end - u);
+        p.k0 = max(at - COST, 0);
+        p.k1 = at + size - COST;
         p.result = p.k0 == 0 && p.k1 == n ? -1 : 2 * w + (u != begin);
-        u += p.k1 - p.k0;
-        return true;
+        u += size;
+        return p.k1 > 0;   // or the part ends before the first block
     }
 };
 

@@ -58,7 +58,7 @@ __global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_ti
     const float tscale = CAP == kCapTurned ? fminf(fabsf(a.scale) / a.softcap * (2.0f * kLog2e), FLT_MAX)
                          : CAP             ? cap_scale(fabsf(a.scale), a.softcap)
                                            : 0.0f;
-    Pieces<R, BK> pieces;
+    Pieces<R, BK, 2> pieces;
     Piece pc;
     if (!pieces.start(a, 1, line)) return;
     int u = pieces.begin;
