@@ -21,7 +21,7 @@ __device__ __forceinline__ bool out_row(const PagedArgs& a, const PagedRecord& r
 // The row of the workspace that holds the i-th result's row r of a head.
 template <int R>
 __device__ __forceinline__ int64_t result_row(const PagedArgs& a, const PagedRecord& rec, int sub, int i, int r) {
-    return ((int64_t)(i == 0 ? rec.slot0 : rec.slot1 + 2 * i) * a.group_heads + sub) * R + r;
+    return ((int64_t)(i == 0 ? rec.slot0 : rec.slot1 + rec.step * i) * a.group_heads + sub) * R + r;
 }
 
 // Few results: as many threads as a row is wide add up its outputs, 256 / W rows
@@ -187,7 +187,9 @@ PagedPlan plan_paged_attention(int32_t dtype, bool e4m3, const PagedArgs& a) {
     if (p.tiles <= kPagedTiles && a.batch <= kPagedTiles && blocks > 1 && units < 2 * wgs && units * (blocks + 8) < 0x7fffffff) {
         p.parts = (int32_t)(wgs < units * blocks ? wgs : units * blocks);
         if (p.parts > kMostParts) p.parts = kMostParts;
-        p.ws_bytes = record_bytes(p.tiles, a.heads_kv / p.group_heads) + (int64_t)p.parts * 2 * p.group_heads * p.rows * (a.d + 2) * 4;
+        const int32_t groups = a.heads_kv / p.group_heads;
+        const int64_t results = p.rows > 16 && cut_by_tiles(a.batch, p.tiles, groups, p.parts) ? p.parts : 2 * p.parts;
+        p.ws_bytes = record_bytes(p.tiles, groups) + results * p.group_heads * p.rows * (a.d + 2) * 4;
     }
     return p;
 }

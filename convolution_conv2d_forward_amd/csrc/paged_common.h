@@ -5,15 +5,15 @@
 // are cut into tiles of R rows, the keys that a tile's rows see into blocks of
 // BU keys: the blocks of the first tokens, then those from the window's first
 // key on.  One workgroup takes a (tile, head) whole where there are many; else
-// the blocks of all tiles and heads form one line, tile after tile and head
-// after head, which is cut into equal parts, a workgroup each, whatever the
+// their blocks are divided (Pieces), most simply as one line, tile after tile and
+// head after head, cut into equal parts, a workgroup each, whatever the
 // sequences' lengths.  (A workgroup may take two heads at once: then "head" is a
-// pair of them.)  A (tile, head) that a cut divides leaves partial results
-// in the workspace, two at most a workgroup (one that its part begins with, one
-// that it ends with), which a second launch joins.
+// pair of them.)  A (tile, head) that is divided leaves partial results in the
+// workspace, two at most a workgroup (one that its part begins with, one that it
+// ends with), which a second launch joins.
 //
 // Lengths and offsets come from the device, so each workgroup of the first launch
-// works the line out for itself; together they leave the second one a record of
+// works the division out for itself; together they leave the second one a record of
 // each (tile, group of heads).
 #pragma once
 
@@ -198,11 +198,8 @@ __device__ __forceinline__ bool find_tile(const PagedArgs& a, int64_t i, int& b,
     return false;
 }
 
-// Parts that a line of `all` blocks (all heads) is cut into, and the first
-// block of one.  Each has `least` blocks or more.
-__device__ __forceinline__ int line_parts(const PagedArgs& a, int all, int least) {
-    return max(min(a.parts, all / least), 1);
-}
+// A line of `all` blocks (all heads) cut into parts: the first block of one, and
+// the part that a block lies in.
 __device__ __forceinline__ int part_begin(int all, int parts, int w) { return (int)((int64_t)all * w / parts); }
 __device__ __forceinline__ int part_of(int all, int parts, int block) {
     return (int)((((int64_t)block + 1) * parts - 1) / all);
@@ -212,10 +209,11 @@ __device__ __forceinline__ int part_of(int all, int parts, int block) {
 // of d for each head of each of two results, then their (running maximum, sum).
 struct PagedRecord {
     int32_t n;             // results to be joined; 0: none
-    int32_t slot0, slot1;  // the first one is at slot0, the i-th other at slot1 + 2 i
+    int32_t slot0, slot1;  // the first one is at slot0, the i-th other at slot1 + step i
+    int32_t step;
     int32_t first, rows;   // the tile's first row of q and, of the sequence's rows from it on, those that there are
     int32_t skip;          // rows of the first token that belong to the tile before
-    int32_t unused[2];
+    int32_t unused;
 };
 struct PagedWs {
     PagedRecord* record;
@@ -225,12 +223,17 @@ struct PagedWs {
 __host__ __device__ __forceinline__ int64_t record_bytes(int64_t tiles, int head_groups) {
     return tiles * head_groups * (int64_t)sizeof(PagedRecord);
 }
+// Whether each tile's keys can be cut by themselves (Pieces).
+__host__ __device__ __forceinline__ bool cut_by_tiles(int batch, int tiles, int head_groups, int parts) {
+    return batch <= 64 && tiles <= 64 && tiles * head_groups <= parts;
+}
 template <int R>
 __device__ __forceinline__ PagedWs paged_ws(const PagedArgs& a) {
     PagedWs w;
     w.record = (PagedRecord*)a.ws;
     w.out = (float*)((char*)a.ws + record_bytes(a.tiles, a.head_groups));
-    w.stat = (f32x2*)(w.out + (int64_t)a.parts * 2 * a.group_heads * R * a.d);
+    const int results = R > 16 && cut_by_tiles(a.batch, a.tiles, a.head_groups, a.parts) ? a.parts : 2 * a.parts;
+    w.stat = (f32x2*)(w.out + (int64_t)results * a.group_heads * R * a.d);
     return w;
 }
 
@@ -242,21 +245,38 @@ struct Piece {
     int result;     // in the workspace; -1 where the piece is all of its (tile, group)
 };
 
-// A (tile, group) counts COST blocks more than it has: what it costs a workgroup
-// to begin another one.  (128-row tiles, chunks of prompts and single tokens:
-// 58.2 us with 0, 55.5 with 2, 55.9 with 3.  Where the workgroups share all of
-// the memory's bandwidth, as with single tokens, 0 is best.)
+// How keys are divided.
+//
+// The line is cut into equal parts, a workgroup a part: it may have the end of
+// one tile's keys, tiles, and the beginning of another's.  A (tile, group) counts
+// COST blocks more than it has: what it costs a workgroup to begin another one.
+// (128-row tiles, chunks of prompts and single tokens: 58.2 us with 0, 55.5 with
+// 2, 55.9 with 3; single tokens share all of the memory's bandwidth, and 0 is
+// best.)
+//
+// BY_TILES (tiles of 64 and 128 rows), where the workgroups suffice for that:
+// each tile's keys are cut by themselves, into equal pieces, a workgroup a piece.
+// The workgroups of an XCD then take tiles of the same head whose pieces begin at
+// the same keys, and find them in its L2.  (A chunk of 2048 tokens over 32768
+// keys: 677 us by the line with 9 in 100 reads found there, 624 with 96.  Tiles of
+// 16 rows have no keys in common, and their pieces come out less equal: a token of
+// 32 sequences of up to 8192 keys 80.6 us by the line, 82.6 by tiles.)
 //
 // Up to 64 sequences and tiles are kept in the lanes of each wave, a tile a lane:
 // no LDS, no barrier, each length and offset read once (a call of a token of 32
 // sequences: 3 us less than by way of LDS).
-template <int R, int BU, int COST>
+template <int R, int BU, int COST, bool BY_TILES>
 struct Pieces {
-    PagedSeq sq;                       // lane's tile: its sequence,
-    int b, t, cum;                     // number, place, blocks of one head before it
+    PagedSeq sq;              // lane's tile: its sequence,
+    int b, t;                 // number and place,
+    int n, cuts, cum;         // its blocks, the pieces they are cut into, pieces (the line: blocks) of one head before
     int tiles, begin, end, w;
+    int pieces;               // of one head
 
-    static __device__ __forceinline__ bool in_lanes(const PagedArgs& a) { return a.batch <= 64 && a.tiles <= 64 && a.first_tile == 0; }
+    static __device__ __forceinline__ bool in_lanes(const PagedArgs& a) {
+        return BY_TILES && a.parts ? cut_by_tiles(a.batch, a.tiles, a.head_groups, a.parts)
+                                   : a.batch <= 64 && a.tiles <= 64 && a.first_tile == 0;
+    }
 
     static __device__ __forceinline__ int sum_before_lane(int v) {
         const int lane = threadIdx.x & 63;
@@ -269,34 +289,59 @@ struct Pieces {
         return s - v;
     }
 
-    // `least`: blocks of a part at least.  False: nothing to do.
-    __device__ __forceinline__ bool start(const PagedArgs& a, int least, PagedLine& l) {
-        int blocks;   // of one head
+    // Cuts each tile's blocks into pieces of T and less, T the least that leaves a
+    // head no more than `most` pieces: a lane tries one, each 2^(1/16) of the one
+    // before, from what an even division would give on; the last one cuts nothing.
+    __device__ __forceinline__ void cut(int most) {
+        const int lane = threadIdx.x & 63;
+        const int all = __builtin_amdgcn_readlane(sum_before_lane(n) + n, 63);
+        const float even = (float)all / (float)most * __builtin_amdgcn_exp2f((float)lane * 0.0625f);
+        const float inv = 1.0f / (lane == 63 ? (float)all : ceilf(even));
+        const auto of = [](int blocks, float inv) { return max((int)ceilf((float)blocks * inv - 0x1p-10f), 1); };
+        int sum = 0;
+        for (int i = 0; i < tiles; ++i) sum += of(__builtin_amdgcn_readlane(n, i), inv);
+        const int best = (int)__builtin_ctzll(__ballot(sum <= most) | 1ull << 63);
+        const float chosen = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, inv), best));
+        cuts = lane < tiles ? of(n, chosen) : 0;
+        cum = sum_before_lane(cuts);
+        pieces = __builtin_amdgcn_readlane(cum + cuts, 63);
+    }
+
+    // False: nothing to do.
+    __device__ __forceinline__ bool start(const PagedArgs& a, PagedLine& l) {
+        begin = 0;
+        end = 1;
         if (in_lanes(a)) {
             const int lane = threadIdx.x & 63;
             PagedSeq s = paged_seq(a, min(lane, a.batch - 1));
             if (lane >= a.batch) s.nq = 0;
-            const int n = min((s.nq * a.group + R - 1) / R, a.tiles), before = sum_before_lane(n);
-            tiles = min(__builtin_amdgcn_readlane(before + n, 63), a.tiles);
+            const int m = min((s.nq * a.group + R - 1) / R, a.tiles), before = sum_before_lane(m);
+            tiles = min(__builtin_amdgcn_readlane(before + m, 63), a.tiles);
             b = 0;
 #pragma unroll
             for (int m = 32; m; m >>= 1)
                 if (__shfl(before, b + m, 64) <= lane) b += m;
             t = lane - __shfl(before, b, 64);
             sq = PagedSeq{__shfl(s.first, b, 64), __shfl(s.nq, b, 64), __shfl(s.nk, b, 64)};
-            const int mine = lane < tiles ? max(key_blocks<R, BU>(a, sq, t * R).n, 1) + COST : 0;
+            n = lane < tiles ? max(key_blocks<R, BU>(a, sq, t * R).n, 1) : 0;
+        }
+        if (!a.parts) return true;
+        int blocks;   // of one head
+        if (BY_TILES && in_lanes(a)) {
+            cut(a.parts / a.head_groups);
+            keep(a, l, 0, 0);
+            const int all = pieces * a.head_groups;
+            w = (int)xcd_remap(blockIdx.x, (uint32_t)all);
+            return (int)blockIdx.x < all;
+        } else if (in_lanes(a)) {
+            const int mine = n ? n + COST : 0;
             cum = sum_before_lane(mine);
             blocks = __builtin_amdgcn_readlane(cum + mine, 63);
-        } else if (a.parts) {
+        } else {
             tiles = make_line<R, BU, COST>(a, l);
             blocks = l.cum[tiles];
         }
-        if (!a.parts) {
-            begin = 0;
-            end = 1;
-            return true;
-        }
-        const int all = blocks * a.head_groups, parts = line_parts(a, all, least);
+        const int all = blocks * a.head_groups, parts = max(min(a.parts, all), 1);
         keep(a, l, all, parts);
         w = (int)xcd_remap(blockIdx.x, (uint32_t)parts);
         begin = __builtin_amdgcn_readfirstlane(part_begin(all, parts, w));
@@ -310,34 +355,40 @@ struct Pieces {
         const int j = (int)(blockIdx.x + threadIdx.x * gridDim.x), units = a.tiles * a.head_groups;
         const int i = j / a.head_groups, h = j - i * a.head_groups;
         if (threadIdx.x >= 64) return;
-        PagedSeq s;
-        int c = 0, place = 0;
+        PagedRecord r{};
+        PagedSeq s{};
+        int place = 0, blocks = 0, c = 0;
         if (in_lanes(a)) {
             const int from = min(i, 63);
-            s = PagedSeq{__shfl(sq.first, from, 64), __shfl(sq.nq, from, 64), __shfl(sq.nk, from, 64)};
-            c = __shfl(cum, from, 64);
+            s = PagedSeq{__shfl(sq.first, from, 64), __shfl(sq.nq, from, 64), 0};
             place = __shfl(t, from, 64);
+            blocks = __shfl(n, from, 64);
+            c = __shfl(cum, from, 64);
+            if (BY_TILES) r.n = __shfl(cuts, from, 64);   // none past the last tile
         } else if (i < tiles) {
             const int k = last_at_most(a.batch, [&](int m) { return l.first[m]; }, i);
             s = paged_seq(a, k);
-            c = l.cum[i];
             place = i - l.first[k];
+            c = l.cum[i];
+            blocks = l.cum[i + 1] - c - COST;
+        }
+        if (BY_TILES && in_lanes(a)) {
+            r.slot0 = r.slot1 = h * pieces + c;
+            r.step = 1;
+        } else if (i < tiles) {
+            const int from = c * a.head_groups + h * (blocks + COST);
+            const int p0 = part_of(all, parts, from + COST), p1 = part_of(all, parts, from + COST + blocks - 1);
+            r.n = p1 - p0 + 1;
+            r.slot0 = 2 * p0 + (part_begin(all, parts, p0) < from);
+            r.slot1 = 2 * p0;
+            r.step = 2;
         }
         if (j >= units) return;
-        PagedRecord r{};
-        if (i < tiles) {
-            const int n = max(key_blocks<R, BU>(a, s, place * R).n, 1), from = c * a.head_groups + h * (n + COST);
-            const int p0 = part_of(all, parts, from + COST), p1 = part_of(all, parts, from + COST + n - 1);
-            const int token = token_of(a, place * R);
-            if (p1 > p0) {
-                r.n = p1 - p0 + 1;
-                r.slot0 = 2 * p0 + (part_begin(all, parts, p0) < from);
-                r.slot1 = 2 * p0;
-                r.first = s.first + token;
-                r.skip = place * R - token * a.group;
-                r.rows = s.nq * a.group - place * R;
-            }
-        }
+        if (r.n == 1) r.n = 0;   // written whole
+        const int token = token_of(a, place * R);
+        r.first = s.first + token;
+        r.skip = place * R - token * a.group;
+        r.rows = s.nq * a.group - place * R;
         paged_ws<R>(a).record[j] = r;
     }
 
@@ -368,27 +419,38 @@ struct Pieces {
             u = end;
             return true;
         }
-        const int heads = a.head_groups;
-        int c, n;
+        const int heads = a.head_groups, lane = threadIdx.x & 63;
+        if (BY_TILES && in_lanes(a)) {
+            p.h = w / pieces;
+            const int at = w - p.h * pieces, i = __builtin_popcountll(__ballot(lane < tiles && cum <= at)) - 1;
+            from_lanes(i, p);
+            const int of = __builtin_amdgcn_readlane(cuts, i), k = at - __builtin_amdgcn_readlane(cum, i);
+            const int blocks = __builtin_amdgcn_readlane(n, i), size = blocks / of, rest = blocks - size * of;
+            p.k0 = size * k + min(k, rest);
+            p.k1 = p.k0 + size + (k < rest);
+            p.result = of == 1 ? -1 : w;
+            u = end;
+            return true;
+        }
+        int c, blocks;
         if (in_lanes(a)) {
-            const int lane = threadIdx.x & 63;
             const int i = __builtin_popcountll(__ballot(lane < tiles && cum * heads <= u)) - 1;
             from_lanes(i, p);
             c = __builtin_amdgcn_readlane(cum, i);
-            n = max(key_blocks<R, BU>(a, p.sq, p.t * R).n, 1);
+            blocks = __builtin_amdgcn_readlane(n, i);
         } else {
             const int i = __builtin_amdgcn_readfirstlane(last_at_most(tiles, [&](int j) { return l.cum[j] * heads; }, u));
             c = __builtin_amdgcn_readfirstlane(l.cum[i]);
-            n = __builtin_amdgcn_readfirstlane(l.cum[i + 1]) - c - COST;
+            blocks = __builtin_amdgcn_readfirstlane(l.cum[i + 1]) - c - COST;
             p.b = __builtin_amdgcn_readfirstlane(last_at_most(a.batch, [&](int j) { return l.first[j]; }, i));
             p.t = i - __builtin_amdgcn_readfirstlane(l.first[p.b]);
             p.sq = paged_seq(a, p.b);
         }
-        p.h = (u - c * heads) / (n + COST);
-        const int at = u - c * heads - p.h * (n + COST), size = min(n + COST - at, end - u);
+        p.h = (u - c * heads) / (blocks + COST);
+        const int at = u - c * heads - p.h * (blocks + COST), size = min(blocks + COST - at, end - u);
         p.k0 = max(at - COST, 0);
         p.k1 = at + size - COST;
-        p.result = p.k0 == 0 && p.k1 == n ? -1 : 2 * w + (u != begin);
+        p.result = p.k0 == 0 && p.k1 == blocks ? -1 : 2 * w + (u != begin);
         u += size;
         return p.k1 > 0;   // or the part ends before the first block
     }

@@ -109,9 +109,9 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4, GH>::NW), (PagedRows<T, 
     sp.cap = a.softcap;
     sp.scale = a.softcap > 0.0f ? cap_scale(a.scale, a.softcap) : a.scale * kLog2e;
 
-    Pieces<16, BU, 0> pieces;
+    Pieces<16, BU, 0, false> pieces;
     Piece pc;
-    if (!pieces.start(a, 1, line)) return;
+    if (!pieces.start(a, line)) return;
     int u = pieces.begin;
     while (pieces.next(kernel_args(), line, u, pc)) {
         const PagedArgs& a = kernel_args();

@@ -58,9 +58,9 @@ __global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_ti
     const float tscale = CAP == kCapTurned ? fminf(fabsf(a.scale) / a.softcap * (2.0f * kLog2e), FLT_MAX)
                          : CAP             ? cap_scale(fabsf(a.scale), a.softcap)
                                            : 0.0f;
-    Pieces<R, BK, 2> pieces;
+    Pieces<R, BK, 2, true> pieces;
     Piece pc;
-    if (!pieces.start(a, 1, line)) return;
+    if (!pieces.start(a, line)) return;
     int u = pieces.begin;
     while (pieces.next(kernel_args(), line, u, pc)) {
         const PagedArgs& a = kernel_args();

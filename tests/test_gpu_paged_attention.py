@@ -284,6 +284,22 @@ def test_many_sequences(batch, dtype, cache):
 
 
 @pytest.mark.parametrize("dtype,cache", KINDS)
+@pytest.mark.parametrize("q_len,batch,heads", [(40, 36, 32), (40, 80, 16), (100, 30, 36), (1, 80, 32)])
+def test_enough_rows_for_whole_tiles(q_len, batch, heads, dtype, cache):
+    """Two rounds of workgroups and more: no tile is divided."""
+    lens = [(37 * i) % 90 + q_len // 2 for i in range(batch)]
+    _check([q_len - i % 3 if q_len > 1 else 1 for i in range(batch)], lens, heads, heads, 32, 16, dtype, cache)
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+@pytest.mark.parametrize("c", [{}, dict(window=200, sinks=70)], ids=str)
+@pytest.mark.parametrize("q_lens", [[900, 40, 1], [0, 700, 3]], ids=str)
+def test_more_tiles_than_lanes(q_lens, c, dtype, cache):
+    """Tiles of a few sequences that are more than 64, and divided."""
+    _check(q_lens, [1000, 700, 90], 24, 2, 32, 16, dtype, cache, **c)
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
 def test_large_scores(dtype, cache):
     """Scores of thousands: weights of 0 and 1, no overflow; scores all equal to a large negative number."""
     out = _check([40, 1], [200, 200], 2, 1, 64, 16, dtype, cache, sharp=0.0)
