@@ -136,6 +136,9 @@ __global__ __launch_bounds__(256) void paged_join_many(PagedArgs a) {
 template <typename T, int R, int DP>
 hipError_t join(const PagedArgs& a, hipStream_t s) {
     const int64_t units = (int64_t)a.tiles * a.heads_kv;
+    // 8 results a (tile, head group) or more: many.  (A token over 131071 keys,
+    // 128 results each: 61.4 us with many, 77.8 with few; 16 sequences of 80 rows, 8
+    // results each at most: 39.8 with many, 33.4 with few.)
     if (a.parts >= 8 * (int64_t)a.tiles * a.head_groups)
         paged_join_many<T, R, DP><<<dim3((uint32_t)(units * R)), dim3(256), 0, s>>>(a);
     else
@@ -156,7 +159,11 @@ PagedPlan plan_paged_attention(int32_t dtype, bool e4m3, const PagedArgs& a) {
     PagedPlan p{};
     const bool f32 = dtype == CONV_DTYPE_F32;
     const int64_t cus = device_cu_count(), all = (int64_t)a.tokens * a.group, seqs = a.batch < a.tokens ? a.batch : a.tokens;
-    p.rows = all <= 16 * seqs ? 16 : all >= 96 * seqs || (f32 && a.d > 128) ? 128 : 64;
+    // As many rows as a sequence has on average.  (16 sequences of up to 4096 keys,
+    // 4 heads of 128 bf16, 20 rows each: 32.9 us in tiles of 16, 26.6 in 64; 64
+    // rows: 28.7 in 64, 29.4 in 128; 80 rows: 33.5 and 31.5.)  Beyond 128 wide, two
+    // stages of 64 fp32 keys do not fit in LDS.
+    p.rows = all <= 16 * seqs ? 16 : all > 64 * seqs || (f32 && a.d > 128) ? 128 : 64;
     // A sequence's rows come in groups: what its last tile may lack is a multiple
     // of what the group has in common with a tile.
     p.tiles = (int32_t)((all + seqs * (p.rows - std::gcd(a.group, p.rows))) / p.rows);

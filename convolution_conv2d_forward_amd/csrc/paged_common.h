@@ -250,9 +250,9 @@ struct Piece {
 // The line is cut into equal parts, a workgroup a part: it may have the end of
 // one tile's keys, tiles, and the beginning of another's.  A (tile, group) counts
 // COST blocks more than it has: what it costs a workgroup to begin another one.
-// (128-row tiles, chunks of prompts and single tokens: 58.2 us with 0, 55.5 with
-// 2, 55.9 with 3; single tokens share all of the memory's bandwidth, and 0 is
-// best.)
+// (128-row tiles, chunks of prompts and single tokens, by the line: 58.2 us with
+// 0, 55.5 with 2, 55.9 with 3; tiles of 16 rows share all of the memory's
+// bandwidth, and 0 is best.)
 //
 // BY_TILES (tiles of 64 and 128 rows), where the workgroups suffice for that:
 // each tile's keys are cut by themselves, into equal pieces, a workgroup a piece.
