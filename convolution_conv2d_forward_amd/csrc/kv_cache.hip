@@ -174,6 +174,9 @@ __global__ __launch_bounds__(256) void kv_load_vec(KvArgs a) {
     }
 }
 
+// A grid's workgroups, whatever its dimensions, at most.
+constexpr int64_t kMostGrid = (int64_t)1 << 22;
+
 // Workgroups for so many waves: as many as run at once, or fewer.
 uint32_t grid_of(int64_t waves) {
     const int64_t most = (int64_t)device_cu_count() * 8, n = (waves + 3) / 4;
@@ -183,7 +186,8 @@ uint32_t grid_of(int64_t waves) {
 template <typename T, bool E4, int LPH>
 hipError_t store_vec(const KvArgs& a, hipStream_t s) {
     const int parts = (2 * a.heads + 64 / LPH * UN - 1) / (64 / LPH * UN);
-    kv_store_vec<T, E4, LPH><<<dim3(grid_of(a.tokens), (uint32_t)parts), dim3(256), 0, s>>>(a);
+    const uint32_t x = grid_of(a.tokens), most = (uint32_t)(kMostGrid / parts);
+    kv_store_vec<T, E4, LPH><<<dim3(x < most ? x : most, (uint32_t)parts), dim3(256), 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -202,9 +206,9 @@ hipError_t store(bool vec, const KvArgs& a, hipStream_t s) {
 template <typename T, bool E4, int LPH>
 hipError_t load_vec(const KvArgs& a, hipStream_t s) {
     const int parts = (2 * a.heads + 64 / LPH * UN - 1) / (64 / LPH * UN);
-    const uint32_t x = grid_of(a.kv_len);
-    const int64_t most = ((int64_t)1 << 22) / ((int64_t)x * parts) + 1;
-    kv_load_vec<T, E4, LPH><<<dim3(x, (uint32_t)parts, (uint32_t)(a.batch < most ? a.batch : most)), dim3(256), 0, s>>>(a);
+    const uint32_t all = grid_of(a.kv_len), each = (uint32_t)(kMostGrid / parts), x = all < each ? all : each;
+    const uint32_t most = each / x, z = (uint32_t)a.batch < most ? (uint32_t)a.batch : most;
+    kv_load_vec<T, E4, LPH><<<dim3(x, (uint32_t)parts, z < 65535 ? z : 65535), dim3(256), 0, s>>>(a);
     return hipGetLastError();
 }
 

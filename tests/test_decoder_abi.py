@@ -162,6 +162,19 @@ def test_block_norm_refusals():
     assert f(rows=0, y=None) == m.CONV_OK
 
 
+def test_tensors_of_no_gpu_are_refused():
+    """The binding's check of a call's tensors: none of them may lie elsewhere than on the call's device."""
+    cc()
+    from convolution_conv2d_forward_amd._marshal import on_device
+    x = torch.zeros(2, 8)
+    with pytest.raises((ValueError, TypeError), match="x"):
+        on_device(0, x, "x", torch.float32, (2, 8), None)
+    for args in ((x, "x", torch.float32, (2, 8), None), (-1, x, "x", torch.float32, (2, 8), None), (0, x)):
+        with pytest.raises(TypeError):
+            on_device(*args)
+    assert on_device(0, None, "x", torch.float32, (2, 8), None) is None
+
+
 def test_reference_by_hand():
     codes, e = quantise64(torch.tensor([[448.0, 1.0, -0.3], [449.0, 1.0, 27.0], [0.0, 0.0, 0.0], [1.0, math.inf, math.nan]]))
     assert e.tolist() == [0, 1, -117, -8]

@@ -210,3 +210,20 @@ def test_pages_beyond_32_bit_offsets():
         codes, e = quantise64(src)
         for t, slot in enumerate(slots):
             _same(got[0, slot], torch.ldexp(codes[t], e[t][:, None]))
+
+
+@pytest.mark.parametrize("d", [8, 256, 5])
+def test_many_heads(d):
+    """As many heads as a descriptor takes, stored and brought back as they are."""
+    m, heads, ps = cc(), 1 << 16, 2
+    desc = m.kv_cache_desc_create(m.make_kv_cache_params(heads, d, ps, dtype="bf16"))
+    g = torch.Generator(device="cuda").manual_seed(0)
+    k, v = (torch.randn(3, heads, d, generator=g, device="cuda").to(torch.bfloat16) for _ in "kv")
+    pages = [torch.zeros(3, ps, heads, d, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    m.kv_cache_store(desc, k, v, ints([5, 0, 4]), *pages)
+    out = [torch.zeros(2, 3, heads, d, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    m.kv_cache_load(desc, ints([[2, 0], [0, 3]]), ints([3, 4]), *pages, None, None, *out)
+    for x, page, y in zip((k, v), pages, out):
+        assert torch.equal(page.view(6, heads, d)[[5, 0, 4]], x) and not page.view(6, heads, d)[[1, 2, 3]].any()
+        assert torch.equal(y[0], x[[2, 0, 1]]) and torch.equal(y[1, 0], x[1]) and not y[1, 1:].any()
