@@ -275,6 +275,24 @@ def test_long_caches_and_same_results_twice(dtype, cache):
     assert torch.equal(out, _run(desc, q.cuda(), _offsets(q_lens), lens, table.cuda(), dev))
 
 
+@pytest.mark.parametrize("cache,d", [("bf16", 8), ("e4m3", 16)])
+@pytest.mark.parametrize("q_len,tol", [(1, 2.0 ** -6), (20, 2.0 ** -4)])
+def test_keys_up_to_the_limit(q_len, tol, cache, d):
+    """2^30 keys, one page over and over: what attention over that page gives (the last new tokens, which see a few keys
+    less, too).  A lane adds up to 2^17 weights (single tokens) or 2^18.5 (chunks) in fp32, and as many products: each
+    addition is off by 2^-24 of the sum, twice."""
+    ps = 4096
+    got, values = random_cache(2, ps, 1, d, "bf16", cache, 5)
+    table = torch.ones(1, (1 << 30) // ps, dtype=torch.int32)
+    q = torch.randn(q_len, 1, d, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16)
+    dev = [None if got[n] is None else got[n].cuda() for n in ("k", "v", "ks", "vs")]
+    out = _run(_desc(1, 1, d, ps, dict(dtype="bf16", cache=cache)), q.cuda(), [0, q_len], [1 << 30], table.cuda(), dev)
+    k, v = values["k"][1, :, 0], values["v"][1, :, 0]
+    w = torch.softmax(d ** -0.5 * q[:, 0].double() @ k.T, 1)
+    bound = tol * (w @ v.abs()) + 2.0 ** -7 * (w @ v.abs())   # the weights' and the output's own rounding
+    assert ((out[:, 0].double().cpu() - w @ v).abs() <= bound).all()
+
+
 @pytest.mark.parametrize("dtype,cache", KINDS)
 @pytest.mark.parametrize("batch", [70, 1100])
 def test_many_sequences(batch, dtype, cache):
