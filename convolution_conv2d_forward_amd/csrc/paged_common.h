@@ -297,12 +297,14 @@ struct Pieces {
         const int all = __builtin_amdgcn_readlane(sum_before_lane(n) + n, 63);
         const float even = (float)all / (float)most * __builtin_amdgcn_exp2f((float)lane * 0.0625f);
         const float inv = 1.0f / (lane == 63 ? (float)all : ceilf(even));
-        const auto of = [](int blocks, float inv) { return max((int)ceilf((float)blocks * inv - 0x1p-10f), 1); };
-        int sum = 0;
-        for (int i = 0; i < tiles; ++i) sum += of(__builtin_amdgcn_readlane(n, i), inv);
-        const int best = (int)__builtin_ctzll(__ballot(sum <= most) | 1ull << 63);
+        const auto of = [](float blocks, float inv) { return fmaxf(ceilf(__builtin_fmaf(blocks, inv, -0x1p-10f)), 1.0f); };
+        float sum = 0.0f;
+        const int blocks = __builtin_bit_cast(int, (float)n);
+#pragma unroll 4
+        for (int i = 0; i < tiles; ++i) sum += of(__builtin_bit_cast(float, __builtin_amdgcn_readlane(blocks, i)), inv);
+        const int best = (int)__builtin_ctzll(__ballot(sum <= (float)most) | 1ull << 63);
         const float chosen = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, inv), best));
-        cuts = lane < tiles ? of(n, chosen) : 0;
+        cuts = lane < tiles ? (int)of((float)n, chosen) : 0;
         cum = sum_before_lane(cuts);
         pieces = __builtin_amdgcn_readlane(cum + cuts, 63);
     }
