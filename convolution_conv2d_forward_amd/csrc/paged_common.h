@@ -492,6 +492,14 @@ __device__ __forceinline__ float value_at(const PagedArgs& a, const int32_t* tab
     return to_f32(((const T*)row)[e]);
 }
 
+// 16 bits of a weight are two numbers of bf16: what one holds of it, cut off, and
+// the rest, rounded.  Both are above zero where the weight is (the rest has 2^-20
+// of it more), or a seen infinity would meet a zero or both signs and become NaN.
+__device__ __forceinline__ float weight_part(float w, bool rest) {
+    const float cut = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, w) & 0xffff0000u);
+    return rest ? __builtin_fmaf(w, 0x1p-20f, w - cut) : cut;
+}
+
 // Few rows a tile (paged_rows.h) or 64 or 128 (paged_tile.h).
 template <typename T, bool E4>
 hipError_t launch_paged_rows(const PagedArgs& a, hipStream_t s);

@@ -222,15 +222,11 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4, GH>::NW), (PagedRows<T, 
 #pragma unroll
             for (int d = 0; d < OUT; ++d) o[d] *= fade;
             if constexpr (sizeof(T) == 2) {
-                // 16 bits of the weights, in two parts above zero, as in
-                // attention_rows.
                 bf16x8 fp, fl;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float w = p[j >> 2][j & 3];
-                    const float cut = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, w) & 0xffff0000u);
-                    fp[j] = (bf16)cut;
-                    fl[j] = (bf16)__builtin_fmaf(w, 0x1p-20f, w - cut);
+                    fp[j] = (bf16)weight_part(p[j >> 2][j & 3], false);
+                    fl[j] = (bf16)weight_part(p[j >> 2][j & 3], true);
                 }
 #pragma unroll
                 for (int c = 0; c < VC; ++c)

@@ -10,12 +10,20 @@ namespace conv2d {
 
 namespace {
 
+// The sum of lane l's and lane l ^ 16's.
+__device__ __forceinline__ float both_rows(float x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x),
+                                                    false, false);
+    return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+
 // attention_tile's work on pages: a workgroup of four waves takes 128 of the
 // rows (new token, head of the group) that share a key head, or 64 with two
 // waves a row group (KW = 2), and walks blocks of 64 keys (fp32: 32 or 64).
 // Both products are transposed, S^T = K Q^T and O^T = V^T P^T, in 32x32 steps; a
 // lane keeps the scores of one row; the running maximum is moved only when it
-// rises by more than 8; bf16 weights are rounded before their product.
+// rises by more than 8; bf16 weights are rounded before their product, but for
+// sequences of up to 16 rows.
 //
 // A lane looks up the page of one key of a block, a block ahead, and forms its
 // place; the threads that copy a key's row get it by exchange.  Pages of T go
@@ -72,10 +80,14 @@ __global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_ti
         const KeyBlocks blocks = key_blocks<R, BK>(a, sq, pc.t * R);
         if (blocks.n == 0) last = first;   // no row sees a key
         const int rows = sq.nq * a.group;
+        // A sequence of so few rows keeps 16 bits of its weights, as in paged_rows,
+        // whatever else is in the batch: lanes 16 .. 31 take rows 0 .. 15 again, with
+        // the weights' second parts, and add their outputs at the end.
+        const bool fine = HALF && rows <= 16;
 
         // This lane's row; keys that some and that all rows of the wave see
         // (first tokens apart), and those that all of the workgroup see.
-        const int row = pc.t * R + wave % C::RG * 32 + n;
+        const int row = pc.t * R + wave % C::RG * 32 + (fine ? n & 15 : n);
         const bool live = row < rows;
         const int qi = live ? token_of(a, row) : 0, hq = h * a.group + (live ? row - qi * a.group : 0);
         int lo, hi, w_lo, w_hi, f_lo, f_hi, all_lo, all_hi, unused;
@@ -205,144 +217,158 @@ __global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_ti
                 issue(p, 0);
             }
         }
-        for (int i = first, stage = 0; i < last; ++i, stage ^= 1) {
-            const int k0 = key0(i);
-            // The wave's part of the block.
-            const int kw = k0 + kpart * 32 * TK;
-            const uint32_t at0 = lds0 + (stage * C::STAGE + kpart * 32 * TK * CPR) * 16;
-            uint32_t k_at = at0 + C::k_at(lane), v_at = at0 + C::v_at(lane);
-            asm volatile("" : "+v"(k_at), "+v"(v_at));   // likewise
-            const bool search = mixed(i, there);
-            if constexpr (!E4) {
-                wait_vmem<0>();   // this block's copies have landed
-                if (search) {
-                    // This thread's own chunks of V.
-                    if (i == first) __syncthreads();   // lbad is set
+        // The blocks.  One loop for weights of one part and one for two: with a branch
+        // in the loop exponentials and products do not overlap across it (chunks
+        // among single tokens 58.4 us, 56.2 with two loops, 55.2 all of one part; under a
+        // window 40.8, 39.1, 38.6).
+        const auto walk = [&](auto parts) {
+            for (int i = first, stage = 0; i < last; ++i, stage ^= 1) {
+                const int k0 = key0(i);
+                // The wave's part of the block.
+                const int kw = k0 + kpart * 32 * TK;
+                const uint32_t at0 = lds0 + (stage * C::STAGE + kpart * 32 * TK * CPR) * 16;
+                uint32_t k_at = at0 + C::k_at(lane), v_at = at0 + C::v_at(lane);
+                asm volatile("" : "+v"(k_at), "+v"(v_at));   // likewise
+                const bool search = mixed(i, there);
+                if constexpr (!E4) {
+                    wait_vmem<0>();   // this block's copies have landed
+                    if (search) {
+                        // This thread's own chunks of V.
+                        if (i == first) __syncthreads();   // lbad is set
 #pragma unroll
-                    for (int j = 0; j < CP; ++j) {
-                        const int r = tid / CPR + j * (256 / CPR);
-                        u32x4& chunk = lds[stage * C::STAGE + BK * CPR + j * 256 + tid];
-                        if (((tid % CPR) ^ C::swizzle(r)) < chunks) chunk = cleaned(chunk, i);
+                        for (int j = 0; j < CP; ++j) {
+                            const int r = tid / CPR + j * (256 / CPR);
+                            u32x4& chunk = lds[stage * C::STAGE + BK * CPR + j * 256 + tid];
+                            if (((tid % CPR) ^ C::swizzle(r)) < chunks) chunk = cleaned(chunk, i);
+                        }
                     }
                 }
-            }
-            __syncthreads();
-            const uint64_t now = there;
-            if constexpr (E4) {
-                if (i + 1 < last) commit(i + 1, there1, stage ^ 1);
-                there = there1;
-                if (i + 2 < last) {
-                    const KeyPlace p = place(i + 2, there2);
-                    fetch(p);
-                    there1 = there2;
+                __syncthreads();
+                const uint64_t now = there;
+                if constexpr (E4) {
+                    if (i + 1 < last) commit(i + 1, there1, stage ^ 1);
+                    there = there1;
+                    if (i + 2 < last) {
+                        const KeyPlace p = place(i + 2, there2);
+                        fetch(p);
+                        there1 = there2;
+                    }
+                } else if (i + 1 < last) {
+                    const KeyPlace p = place(i + 1, there);
+                    issue(p, stage ^ 1);
                 }
-            } else if (i + 1 < last) {
-                const KeyPlace p = place(i + 1, there);
-                issue(p, stage ^ 1);
-            }
-            if (kw >= w_hi || (kw + 32 * TK <= w_lo && kw >= a.sinks)) continue;   // none of the wave's rows sees a key
+                if (kw >= w_hi || (kw + 32 * TK <= w_lo && kw >= a.sinks)) continue;   // none of the wave's rows sees a key
 
-            f32x16 s[TK] = {};
-#pragma unroll
-            for (int t = 0; t < TK; ++t)
-#pragma unroll
-                for (int j = 0; j < KS; ++j)
-                    s[t] = mfma32_step<T>(*lds_ptr<const lds_u32x4>((k_at ^ 32 * j) + t * 512 * CPR), fq[j], s[t]);
-            const float a1 = PLAIN ? scale : TURNED ? -2.0f * cap : 1.0f, a0 = TURNED ? cap : 0.0f;
-            if (CAP) {
+                f32x16 s[TK] = {};
 #pragma unroll
                 for (int t = 0; t < TK; ++t)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        s[t][j] = TURNED ? turned(s[t][j] * tscale) : cap * score_tanh<T>(s[t][j] * tscale) * kLog2e;
-            }
-            // Keys before and past what a row sees, and on no page, each where
-            // some row needs it.  Score register j holds key 32 (j / 16) +
-            // 8 (j / 4 % 4) + j % 4 from 4 g on.
-            constexpr float NEVER = TURNED ? INFINITY : -INFINITY;
-            const auto key = [](int j) { return 32 * (j >> 4) + 8 * (j >> 2 & 3) + (j & 3); };
-            if (kw < f_lo && kw + 32 * TK > a.sinks) {
-                const int from = lo - kw - 4 * g, kept = a.sinks - kw - 4 * g;
+                    for (int j = 0; j < KS; ++j)
+                        s[t] = mfma32_step<T>(*lds_ptr<const lds_u32x4>((k_at ^ 32 * j) + t * 512 * CPR), fq[j], s[t]);
+                const float a1 = PLAIN ? scale : TURNED ? -2.0f * cap : 1.0f, a0 = TURNED ? cap : 0.0f;
+                if (CAP) {
 #pragma unroll
-                for (int j = 0; j < 16 * TK; ++j)
-                    if (key(j) < from && key(j) >= kept) s[j >> 4][j & 15] = NEVER;
-            }
-            if (kw + 32 * TK > f_hi) {
-                const int to = hi - kw - 4 * g;
+                    for (int t = 0; t < TK; ++t)
 #pragma unroll
-                for (int j = 0; j < 16 * TK; ++j)
-                    if (key(j) >= to) s[j >> 4][j & 15] = NEVER;
-            }
-            if (~now != 0) {
-                const uint64_t mine = now >> (kpart * 32 * TK + 4 * g);
-#pragma unroll
-                for (int j = 0; j < 16 * TK; ++j)
-                    if (!(mine >> key(j) & 1)) s[j >> 4][j & 15] = NEVER;
-            }
-            float top = s[0][0];
-#pragma unroll
-            for (int j = 1; j < 16 * TK; ++j) {
-                const float x = s[j >> 4][j & 15];
-                top = TURNED ? fminf(top, x) : fmaxf(top, x);
-            }
-            {
-                float u, v;
-                both_halves(top, u, v);
-                top = (TURNED ? fminf(u, v) : fmaxf(u, v)) * a1 + a0;
-            }
-            if (__ballot(top > m_run + 8.0f)) {
-                const float m_new = fmaxf(m_run, top);
-                const float fade = __builtin_amdgcn_exp2f(m_run - (m_new == -INFINITY ? 0.0f : m_new));
-                m_run = m_new;
-                l_run *= fade;
-#pragma unroll
-                for (int d = 0; d < DT; ++d) o[d] *= fade;
-            }
-            const float base = a0 - (m_run == -INFINITY ? 0.0f : m_run);   // nothing seen yet: every weight is 0
-            bf16x8 p[2 * TK];
-#pragma unroll
-            for (int t = 0; t < 2 * TK; ++t)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float w = __builtin_amdgcn_exp2f(s[t >> 1][8 * (t & 1) + j] * a1 + base);
-                    s[t >> 1][8 * (t & 1) + j] = w;
-                    l_run += w;
-                    if (HALF) p[t][j] = (bf16)w;
+                        for (int j = 0; j < 16; ++j)
+                            s[t][j] = TURNED ? turned(s[t][j] * tscale) : cap * score_tanh<T>(s[t][j] * tscale) * kLog2e;
                 }
-            if constexpr (HALF) {
+                // Keys before and past what a row sees, and on no page, each where
+                // some row needs it.  Score register j holds key 32 (j / 16) +
+                // 8 (j / 4 % 4) + j % 4 from 4 g on.
+                constexpr float NEVER = TURNED ? INFINITY : -INFINITY;
+                const auto key = [](int j) { return 32 * (j >> 4) + 8 * (j >> 2 & 3) + (j & 3); };
+                if (kw < f_lo && kw + 32 * TK > a.sinks) {
+                    const int from = lo - kw - 4 * g, kept = a.sinks - kw - 4 * g;
+#pragma unroll
+                    for (int j = 0; j < 16 * TK; ++j)
+                        if (key(j) < from && key(j) >= kept) s[j >> 4][j & 15] = NEVER;
+                }
+                if (kw + 32 * TK > f_hi) {
+                    const int to = hi - kw - 4 * g;
+#pragma unroll
+                    for (int j = 0; j < 16 * TK; ++j)
+                        if (key(j) >= to) s[j >> 4][j & 15] = NEVER;
+                }
+                if (~now != 0) {
+                    const uint64_t mine = now >> (kpart * 32 * TK + 4 * g);
+#pragma unroll
+                    for (int j = 0; j < 16 * TK; ++j)
+                        if (!(mine >> key(j) & 1)) s[j >> 4][j & 15] = NEVER;
+                }
+                float top = s[0][0];
+#pragma unroll
+                for (int j = 1; j < 16 * TK; ++j) {
+                    const float x = s[j >> 4][j & 15];
+                    top = TURNED ? fminf(top, x) : fmaxf(top, x);
+                }
+                {
+                    float u, v;
+                    both_halves(top, u, v);
+                    top = (TURNED ? fminf(u, v) : fmaxf(u, v)) * a1 + a0;
+                }
+                if (__ballot(top > m_run + 8.0f)) {
+                    const float m_new = fmaxf(m_run, top);
+                    const float fade = __builtin_amdgcn_exp2f(m_run - (m_new == -INFINITY ? 0.0f : m_new));
+                    m_run = m_new;
+                    l_run *= fade;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) o[d] *= fade;
+                }
+                const float base = a0 - (m_run == -INFINITY ? 0.0f : m_run);   // nothing seen yet: every weight is 0
+                bf16x8 p[2 * TK];
 #pragma unroll
                 for (int t = 0; t < 2 * TK; ++t)
 #pragma unroll
-                    for (int d = 0; d < DT; ++d)
-                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(C::vt(v_at, 16 * t, 32 * d), p[t], o[d], 0, 0, 0);
-            } else {
+                    for (int j = 0; j < 8; ++j) {
+                        const float w = __builtin_amdgcn_exp2f(s[t >> 1][8 * (t & 1) + j] * a1 + base);
+                        s[t >> 1][8 * (t & 1) + j] = w;
+                        l_run += w;
+                        if (HALF) p[t][j] = (bf16)(parts ? weight_part(w, n & 16) : w);
+                    }
+                if constexpr (HALF) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
+                    for (int t = 0; t < 2 * TK; ++t)
 #pragma unroll
-                    for (int d = 0; d < DT; ++d)
-                        o[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(C::vt1(v_at, j, 32 * d), s[0][j], o[d], 0, 0, 0);
-            }
-            if (search && lbad[i & 1] == i) {
+                        for (int d = 0; d < DT; ++d)
+                            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(C::vt(v_at, 16 * t, 32 * d), p[t], o[d], 0, 0, 0);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+#pragma unroll
+                        for (int d = 0; d < DT; ++d)
+                            o[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(C::vt1(v_at, j, 32 * d), s[0][j], o[d], 0, 0, 0);
+                }
+                if (search && lbad[i & 1] == i) {
 #pragma unroll 1
-                for (int j = 0; j < 32 * TK; ++j) {
-                    if (kw + j >= sq.nk || !(now >> (kpart * 32 * TK + j) & 1)) continue;
-                    const bool add = kw + j < hi && (kw + j >= lo || kw + j < a.sinks);
+                    for (int j = 0; j < 32 * TK; ++j) {
+                        if (kw + j >= sq.nk || !(now >> (kpart * 32 * TK + j) & 1)) continue;
+                        const bool add = kw + j < hi && (kw + j >= lo || kw + j < a.sinks);
 #pragma unroll 1
-                    for (int e0 = 0; e0 < a.d; e0 += 64) {
-                        const float x = e0 + lane < a.d ? value_at<T, E4>(a, table, h, kw + j, e0 + lane) : 0.0f;
-                        for (uint64_t bad = __ballot(!(fabsf(x) < INFINITY)); bad; bad &= bad - 1) {
-                            const int l = (int)__builtin_ctzll(bad);
-                            const float y = __shfl(x, l, 64);
-                            int at = e0 + l - 4 * g;
-                            asm volatile("" : "+v"(at));   // no comparison is kept in registers across the blocks
+                        for (int e0 = 0; e0 < a.d; e0 += 64) {
+                            const float x = e0 + lane < a.d ? value_at<T, E4>(a, table, h, kw + j, e0 + lane) : 0.0f;
+                            for (uint64_t bad = __ballot(!(fabsf(x) < INFINITY)); bad; bad &= bad - 1) {
+                                const int l = (int)__builtin_ctzll(bad);
+                                const float y = __shfl(x, l, 64);
+                                int at = e0 + l - 4 * g;
+                                asm volatile("" : "+v"(at));   // no comparison is kept in registers across the blocks
 #pragma unroll
-                            for (int d = 0; d < DT; ++d)
+                                for (int d = 0; d < DT; ++d)
 #pragma unroll
-                                for (int q = 0; q < 16; ++q) o[d][q] += add && 32 * d + 8 * (q >> 2) + (q & 3) == at ? y : 0.0f;
+                                    for (int q = 0; q < 16; ++q) o[d][q] += add && 32 * d + 8 * (q >> 2) + (q & 3) == at ? y : 0.0f;
+                            }
                         }
                     }
                 }
             }
+        };
+        if constexpr (HALF) {
+            if (fine)
+                walk(std::true_type{});
+            else
+                walk(std::false_type{});
+        } else {
+            walk(std::false_type{});
         }
         {
             float u, v;
@@ -378,7 +404,13 @@ __global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_ti
                     for (int j = 0; j < 4; ++j) o[d][4 * q + j] = o[d][4 * q + j] * f0 + v[j] * f1;
                 }
         }
-        if (!live) continue;
+        if (fine) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int q = 0; q < 16; ++q) o[d][q] = both_rows(o[d][q]);
+        }
+        if (!live || (fine && n >= 16)) continue;
         const PagedArgs& end = kernel_args();
         const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
         T* op = (T*)end.out + (int64_t)(sq.first + qi) * end.o_s + (int64_t)hq * end.d;

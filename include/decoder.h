@@ -161,9 +161,11 @@ CONV2D_API conv_status_t paged_attention_workspace_bytes(paged_attention_desc_t 
  *               scratch of this call alone until it ends; may be null where
  *               that is 0
  * Sums and softmax statistics are held in fp32; in bf16 the weights meet the
- * values with 16 bits where tokens * heads_q / heads_kv <= 16 * min(batch,
- * tokens) (single tokens, above all), rounded to bf16 elsewhere, and a capped
- * score is off as attention_forward's is.
+ * values with 16 bits in sequences of at most 16 rows of a key head (new tokens *
+ * heads_q / heads_kv: single tokens, above all), whatever else is in the batch,
+ * and in all of them where tokens * heads_q / heads_kv <= 16 * min(batch,
+ * tokens); rounded to bf16 elsewhere.  A capped score is off as
+ * attention_forward's is.
  * Errors: INVALID_ARG for a null or misaligned pointer (16 bytes; lengths,
  * offsets and the table 4), a negative size, tokens or batch beyond 2^30,
  * max_pages * page_size beyond 2^30, or a workspace that is too small;
