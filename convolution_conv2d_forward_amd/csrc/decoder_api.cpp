@@ -411,7 +411,7 @@ conv_status_t paged_attention_forward(paged_attention_desc_t d, int64_t tokens, 
     a.ks = e4m3 ? k_scales : nullptr;
     a.vs = e4m3 ? v_scales : nullptr;
     a.ws = plan.ws_bytes > 0 ? workspace : nullptr;
-    a.tiles = plan.tiles; a.parts = plan.parts;
+    a.tiles = plan.tiles; a.parts = plan.parts; a.long_blocks = plan.long_blocks;
     a.group_heads = plan.group_heads; a.head_groups = a.heads_kv / plan.group_heads;
     return hip_status(launch_paged_attention(p.dtype, e4m3, plan, a, (hipStream_t)stream), "paged_attention");
 }

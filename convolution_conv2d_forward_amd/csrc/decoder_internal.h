@@ -68,6 +68,7 @@ struct PagedArgs {
     int32_t tiles;               // row tiles of all sequences, at most
     int32_t first_tile;          // of this launch, where parts == 0
     int32_t parts;               // workgroups that the keys of all tiles are divided among, at most; 0: one a tile and head
+    int32_t long_blocks;         // > 0: the keys of tiles of more blocks are, and the others have one a tile and head too
     float scale, softcap;
 };
 
@@ -75,7 +76,7 @@ struct PagedArgs {
 struct PagedPlan {
     int32_t rows;                // of a tile: 16, 64 or 128
     int32_t group_heads;
-    int32_t tiles, parts;
+    int32_t tiles, parts, long_blocks;
     int64_t ws_bytes;
 };
 

@@ -27,11 +27,12 @@ __device__ __forceinline__ int64_t result_row(const PagedArgs& a, const PagedRec
 // Few results: as many threads as a row is wide add up its outputs, 256 / W rows
 // a workgroup.
 template <typename T, int R, int DP>
-__global__ __launch_bounds__(256) void paged_join_few(PagedArgs a) {
+__device__ __forceinline__ void join_few(const PagedArgs& a, uint32_t b) {
     constexpr int W = DP / 4, ROWS = 256 / W;
-    const int unit = (int)blockIdx.x / (R / ROWS), r = (int)blockIdx.x % (R / ROWS) * ROWS + (int)threadIdx.x / W;
-    const int sub = unit % a.group_heads, e = ((int)threadIdx.x % W) * 4;
+    const int e = ((int)threadIdx.x % W) * 4;
     const PagedWs w = paged_ws<R>(a);
+    const int unit = (int)(b / (R / ROWS)), r = (int)(b % (R / ROWS)) * ROWS + (int)threadIdx.x / W;
+    const int sub = unit % a.group_heads;
     const PagedRecord rec = w.record[unit / a.group_heads];
     T* out;
     if (!out_row<T>(a, rec, unit % a.heads_kv, r, out) || e >= a.d) return;
@@ -63,6 +64,16 @@ __global__ __launch_bounds__(256) void paged_join_few(PagedArgs a) {
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     *(typename Vec<T>::v4*)(out + e) = from_f32<T>(sum * inv);
+}
+template <typename T, int R, int DP>
+__global__ __launch_bounds__(256) void paged_join_few(PagedArgs a) {
+    join_few<T, R, DP>(a, blockIdx.x);
+}
+// Where only long tiles were divided most records are empty: fewer workgroups
+// look at all of them.
+template <typename T, int R, int DP>
+__global__ __launch_bounds__(256) void paged_join_long(PagedArgs a, uint32_t all) {
+    for (uint32_t b = blockIdx.x; b < all; b += gridDim.x) join_few<T, R, DP>(a, b);
 }
 
 // Many: a workgroup a row.  The results' maxima and sums give each one's
@@ -136,13 +147,18 @@ __global__ __launch_bounds__(256) void paged_join_many(PagedArgs a) {
 template <typename T, int R, int DP>
 hipError_t join(const PagedArgs& a, hipStream_t s) {
     const int64_t units = (int64_t)a.tiles * a.heads_kv;
+    const int64_t few = units * (R / (256 / (DP / 4)));
     // 8 results a (tile, head group) or more: many.  (A token over 131071 keys,
     // 128 results each: 61.4 us with many, 77.8 with few; 16 sequences of 80 rows, 8
     // results each at most: 39.8 with many, 33.4 with few.)
-    if (a.parts >= 8 * (int64_t)a.tiles * a.head_groups)
+    if (R == 16 && a.long_blocks) {
+        const int64_t most = (int64_t)device_cu_count() * 8;
+        paged_join_long<T, 16, DP><<<dim3((uint32_t)(few < most ? few : most)), dim3(256), 0, s>>>(a, (uint32_t)few);
+    } else if (a.parts >= 8 * (int64_t)a.tiles * a.head_groups) {
         paged_join_many<T, R, DP><<<dim3((uint32_t)(units * R)), dim3(256), 0, s>>>(a);
-    else
-        paged_join_few<T, R, DP><<<dim3((uint32_t)(units * (R / (256 / (DP / 4))))), dim3(256), 0, s>>>(a);
+    } else {
+        paged_join_few<T, R, DP><<<dim3((uint32_t)few), dim3(256), 0, s>>>(a);
+    }
     return hipGetLastError();
 }
 
@@ -189,10 +205,22 @@ PagedPlan plan_paged_attention(int32_t dtype, bool e4m3, const PagedArgs& a) {
     // of 8192 tokens, two rounds of them: 364 us divided, 316 whole; one of 4096,
     // one round: 114 and 141.  A token of 128 sequences of up to 2048 keys, two
     // rounds: 149 and 143; of 192, one and a half: 122 and 135.)
+    //
+    // Of more tiles of 16 rows those of more than 2048 keys are, since one sequence
+    // may be longer than all others together; on half of the workgroups that run at
+    // once, while the others take whole tiles.  (A token of 256 sequences of up to
+    // 2048 keys, 32 heads over 8 of 128 E4M3, and of 131071 keys in one of them: 222
+    // us, 3273 whole, 204 with all keys on the line.  Where no sequence is long but
+    // the table has room for it, 5 to 10 us are lost: 127 and 122 at up to 1900 keys;
+    // with all keys on the line 465 for 276 at up to 600 of 32 heads of 64 bf16.)
     const int64_t wgs = cus * per_cu, units = (int64_t)p.tiles * (a.heads_kv / p.group_heads);
     const int64_t blocks = ((int64_t)a.max_pages * a.page_size.d + keys - 1) / keys;
-    if (p.tiles <= kPagedTiles && a.batch <= kPagedTiles && blocks > 1 && units < 2 * wgs && units * (blocks + 8) < 0x7fffffff) {
-        p.parts = (int32_t)(wgs < units * blocks ? wgs : units * blocks);
+    const bool many = units >= 2 * wgs;
+    const int64_t whole = many && p.rows == 16 ? 2048 / keys : 1;   // blocks
+    if (p.tiles <= kPagedTiles && a.batch <= kPagedTiles && blocks > whole && (!many || p.rows == 16) && units <= 128 * wgs &&
+        units * (blocks + 8) < 0x7fffffff) {
+        if (many) p.long_blocks = (int32_t)whole;
+        p.parts = (int32_t)(many ? wgs / 2 : wgs < units * blocks ? wgs : units * blocks);
         if (p.parts > kMostParts) p.parts = kMostParts;
         const int32_t groups = a.heads_kv / p.group_heads;
         const int64_t results = p.rows > 16 && cut_by_tiles(a.batch, p.tiles, groups, p.parts) ? p.parts : 2 * p.parts;

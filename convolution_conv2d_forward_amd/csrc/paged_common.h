@@ -122,6 +122,9 @@ __device__ __forceinline__ int last_at_most(int n, F t, int x) {
     return lo;
 }
 
+// Whether a tile of n blocks is on the line.
+__device__ __forceinline__ bool on_line(const PagedArgs& a, int n) { return n > a.long_blocks; }
+
 // Fills the line; returns the number of tiles.  A tile without keys counts a
 // block: its rows are zeros that someone has to write.  Offsets that do not
 // ascend may make more tiles than the host has counted: those are left out.
@@ -149,7 +152,8 @@ __device__ __forceinline__ int make_line(const PagedArgs& a, PagedLine& l) {
         n[i] = 0;
         if (t < tiles) {
             const int b = last_at_most(a.batch, [&](int j) { return l.first[j]; }, t);
-            n[i] = max(key_blocks<R, BU>(a, paged_seq(a, b), (t - l.first[b]) * R).n, 1) + COST;
+            n[i] = max(key_blocks<R, BU>(a, paged_seq(a, b), (t - l.first[b]) * R).n, 1);
+            n[i] = on_line(a, n[i]) ? n[i] + COST : 0;
         }
         sum += n[i];
     }
@@ -262,6 +266,9 @@ struct Piece {
 // 16 rows have no keys in common, and their pieces come out less equal: a token of
 // 32 sequences of up to 8192 keys 80.6 us by the line, 82.6 by tiles.)
 //
+// Where there are many (tile, group)s, only tiles of more than long_blocks are on
+// the line: the workgroups behind its parts take one of the others each.
+//
 // Up to 64 sequences and tiles are kept in the lanes of each wave, a tile a lane:
 // no LDS, no barrier, each length and offset read once (a call of a token of 32
 // sequences: 3 us less than by way of LDS).
@@ -327,7 +334,7 @@ struct Pieces {
             sq = PagedSeq{__shfl(s.first, b, 64), __shfl(s.nq, b, 64), __shfl(s.nk, b, 64)};
             n = lane < tiles ? max(key_blocks<R, BU>(a, sq, t * R).n, 1) : 0;
         }
-        if (!a.parts) return true;
+        if (blockIdx.x >= (uint32_t)a.parts) return true;
         int blocks;   // of one head
         if (BY_TILES && in_lanes(a)) {
             cut(a.parts / a.head_groups);
@@ -336,14 +343,15 @@ struct Pieces {
             w = (int)xcd_remap(blockIdx.x, (uint32_t)all);
             return (int)blockIdx.x < all;
         } else if (in_lanes(a)) {
-            const int mine = n ? n + COST : 0;
+            const int mine = on_line(a, n) ? n + COST : 0;
             cum = sum_before_lane(mine);
             blocks = __builtin_amdgcn_readlane(cum + mine, 63);
         } else {
             tiles = make_line<R, BU, COST>(a, l);
             blocks = l.cum[tiles];
         }
-        const int all = blocks * a.head_groups, parts = max(min(a.parts, all), 1);
+        const int all = blocks * a.head_groups, least = max(a.long_blocks / 2, 1);   // blocks of a part
+        const int parts = max(min(a.parts, (all + least - 1) / least), 1);
         keep(a, l, all, parts);
         w = (int)xcd_remap(blockIdx.x, (uint32_t)parts);
         begin = __builtin_amdgcn_readfirstlane(part_begin(all, parts, w));
@@ -351,12 +359,12 @@ struct Pieces {
         return (int)blockIdx.x < parts;
     }
 
-    // Leaves records for the join: those of every gridDim.x-th (tile, head), a
-    // thread each.
+    // Leaves records for the join: those of every a.parts-th (tile, head), a thread
+    // each.
     __device__ __forceinline__ void keep(const PagedArgs& a, const PagedLine& l, int all, int parts) {
-        const int j = (int)(blockIdx.x + threadIdx.x * gridDim.x), units = a.tiles * a.head_groups;
+        const int j = (int)(blockIdx.x + threadIdx.x * (uint32_t)a.parts), units = a.tiles * a.head_groups;
         const int i = j / a.head_groups, h = j - i * a.head_groups;
-        if (threadIdx.x >= 64) return;
+        if (threadIdx.x >= 64 && !a.long_blocks) return;   // fewer suffice
         PagedRecord r{};
         PagedSeq s{};
         int place = 0, blocks = 0, c = 0;
@@ -377,7 +385,7 @@ struct Pieces {
         if (BY_TILES && in_lanes(a)) {
             r.slot0 = r.slot1 = h * pieces + c;
             r.step = 1;
-        } else if (i < tiles) {
+        } else if (i < tiles && on_line(a, blocks)) {
             const int from = c * a.head_groups + h * (blocks + COST);
             const int p0 = part_of(all, parts, from + COST), p1 = part_of(all, parts, from + COST + blocks - 1);
             r.n = p1 - p0 + 1;
@@ -404,10 +412,10 @@ struct Pieces {
     // The piece at `u` (begin at first), and where the next one is.
     __device__ __forceinline__ bool next(const PagedArgs& a, PagedLine& l, int& u, Piece& p) {
         if (u >= end) return false;
-        if (!a.parts) {
-            // The last tiles first: they see the most keys.
+        if (blockIdx.x >= (uint32_t)a.parts) {
+            // A sequence's last tiles first: they see the most keys.
             const int64_t i = (int64_t)a.first_tile + (gridDim.x - 1 - blockIdx.x) / (uint32_t)a.head_groups;
-            p.h = (int)(blockIdx.x % (uint32_t)a.head_groups);
+            p.h = (int)((blockIdx.x - (uint32_t)a.parts) % (uint32_t)a.head_groups);
             if (in_lanes(a)) {
                 if (i >= tiles) return false;
                 from_lanes((int)i, p);
@@ -419,7 +427,7 @@ struct Pieces {
             p.k1 = key_blocks<R, BU>(a, p.sq, p.t * R).n;
             p.result = -1;
             u = end;
-            return true;
+            return a.parts == 0 || !on_line(a, p.k1);
         }
         const int heads = a.head_groups, lane = threadIdx.x & 63;
         if (BY_TILES && in_lanes(a)) {

@@ -369,7 +369,8 @@ __global__ __launch_bounds__((64 * PagedRows<T, DP, E4, GH>::NW), (PagedRows<T, 
 
 template <typename T, int DP, bool E4, int GH>
 hipError_t run(const PagedArgs& a, hipStream_t s) {
-    const uint32_t grid = a.parts ? (uint32_t)a.parts : (uint32_t)a.tiles * (uint32_t)a.head_groups;
+    const uint32_t units = (uint32_t)a.tiles * (uint32_t)a.head_groups;
+    const uint32_t grid = (uint32_t)a.parts + (a.parts && !a.long_blocks ? 0 : units);
     paged_rows<T, DP, E4, GH><<<dim3(grid), dim3(256), 0, s>>>(a);
     return hipGetLastError();
 }

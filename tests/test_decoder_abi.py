@@ -187,3 +187,12 @@ def test_reference_by_hand():
     s = lambda *a: seen64(*a).int().tolist()  # noqa: E731
     assert s(2, 3, 0, 0) == [[1, 1, 0], [1, 1, 1]] and s(3, 2, 0, 0) == [[0, 0], [1, 0], [1, 1]]
     assert s(1, 5, 2, 1) == [[1, 0, 0, 1, 1]] and s(2, 4, 1, 3) == [[1, 1, 1, 0], [1, 1, 1, 1]]
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+@pytest.mark.parametrize("batch", [8, 64, 128, 256, 500, 1024])
+def test_single_tokens_of_any_batch_are_divided(batch, cache):
+    """A long sequence among many short ones has to be cut, or one workgroup reads it alone: such calls have a workspace."""
+    m = cc()
+    d = m.paged_attention_desc_create(m.make_paged_attention_params(32, 8, 128, 16, dtype="bf16", cache_dtype=cache))
+    assert m.paged_attention_workspace_bytes(d, batch, batch, 8192) > 0
