@@ -69,6 +69,53 @@ View pages_view(const void* p, const int64_t* s, int64_t n_pages, int64_t page_s
     return View{(uintptr_t)p, 1, 0, pages_span(s, n_pages, page_size, heads, len) * es};
 }
 
+// A tensor of rows of `len` bytes at three strides (bytes), and its view.
+struct Grid {
+    uintptr_t base;
+    int64_t stride[3], n[3], len;
+    View view;
+};
+
+Grid pages_grid(const void* p, const int64_t* s, int64_t n_pages, int64_t page_size, int64_t heads, int64_t len, int64_t es) {
+    return Grid{(uintptr_t)p, {s[0] * es, s[1] * es, s[2] * es}, {n_pages, page_size, heads}, len * es,
+                pages_view(p, s, n_pages, page_size, heads, len, es)};
+}
+
+// Whether rows of two grids of the same strides and counts overlap, `delta` bytes
+// apart: dimension by dimension from the largest stride on, those differences of
+// the two indices that the smaller strides can still make up for.  They are three
+// at most where the dimensions lie within each other.
+bool rows_meet(const std::pair<int64_t, int64_t>* dims, int count, int64_t delta, int64_t a_len, int64_t b_len) {
+    if (count == 0) return delta < a_len && -delta < b_len;
+    const auto [stride, n] = dims[0];
+    int64_t inner = 0;
+    for (int i = 1; i < count; ++i) inner += dims[i].first * (dims[i].second - 1);
+    const auto floor_div = [](int64_t x, int64_t d) { return x >= 0 ? x / d : -((-x + d - 1) / d); };
+    int64_t lo = -floor_div(inner + b_len - 1 + delta, stride), hi = floor_div(inner + a_len - 1 - delta, stride);
+    if (lo < -(n - 1)) lo = -(n - 1);
+    if (hi > n - 1) hi = n - 1;
+    for (int64_t i = lo; i <= hi; ++i)
+        if (rows_meet(dims + 1, count - 1, delta + i * stride, a_len, b_len)) return true;
+    return false;
+}
+
+// Whether two tensors, each with its dimensions within each other, share memory.
+// Exact where they have the same strides in bytes, as tensors that are interleaved
+// in one buffer have; otherwise by their views.
+bool grids_overlap(const Grid& a, const Grid& b) {
+    if (!views_overlap(a.view, b.view)) return false;
+    std::pair<int64_t, int64_t> dims[3];
+    int count = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (a.n[i] != b.n[i]) return true;
+        if (a.n[i] <= 1) continue;
+        if (a.stride[i] != b.stride[i]) return true;
+        dims[count++] = {a.stride[i], a.n[i]};
+    }
+    std::sort(dims, dims + count, [](const auto& x, const auto& y) { return x.first > y.first; });
+    return rows_meet(dims, count, (int64_t)(b.base - a.base), a.len, b.len);
+}
+
 PageStrides page_strides(const int64_t* s) { return PageStrides{s[0], s[1], s[2]}; }
 
 bool misaligned(const void* p, int64_t bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) != 0; }
@@ -121,18 +168,18 @@ conv_status_t check_kv(const kv_cache_params_t& p, int64_t n_pages, const void* 
     return CONV_OK;
 }
 
-struct KvViews {
-    View pages[4];   // keys, values, their scales
+struct KvGrids {
+    Grid pages[4];   // keys, values, their scales
     int n;
 };
 
-KvViews kv_views(const kv_cache_params_t& p, int64_t n_pages, const void* k_pages, const void* v_pages,
+KvGrids kv_grids(const kv_cache_params_t& p, int64_t n_pages, const void* k_pages, const void* v_pages,
                  const uint8_t* k_scales, const uint8_t* v_scales) {
     const int64_t cs = cache_elem_size(p.cache_dtype), ps = p.page_size, h = p.heads_kv, d = p.head_dim;
-    KvViews v{{pages_view(k_pages, p.k_page_strides, n_pages, ps, h, d, cs),
-               pages_view(v_pages, p.v_page_strides, n_pages, ps, h, d, cs),
-               pages_view(k_scales, p.scale_strides, n_pages, ps, h, 1, 1),
-               pages_view(v_scales, p.scale_strides, n_pages, ps, h, 1, 1)},
+    KvGrids v{{pages_grid(k_pages, p.k_page_strides, n_pages, ps, h, d, cs),
+               pages_grid(v_pages, p.v_page_strides, n_pages, ps, h, d, cs),
+               pages_grid(k_scales, p.scale_strides, n_pages, ps, h, 1, 1),
+               pages_grid(v_scales, p.scale_strides, n_pages, ps, h, 1, 1)},
               p.cache_dtype == KV_CACHE_E4M3 ? 4 : 2};
     return v;
 }
@@ -229,14 +276,14 @@ conv_status_t kv_cache_store(kv_cache_desc_t desc, int64_t tokens, const void* k
     if (!nested(p.k_page_strides, n_pages, ps, h, hd) || !nested(p.v_page_strides, n_pages, ps, h, hd) ||
         (e4m3 && !nested(p.scale_strides, n_pages, ps, h, 1)))
         return fail(CONV_ERR_ALIAS, "elements of the pages share memory");
-    const KvViews out = kv_views(p, n_pages, k_pages, v_pages, k_scales, v_scales);
+    const KvGrids out = kv_grids(p, n_pages, k_pages, v_pages, k_scales, v_scales);
     const View in[3] = {rows_view(k, tokens, p.k_stride, h * hd, es), rows_view(v, tokens, p.v_stride, h * hd, es),
                         flat_view(slots, 4 * tokens)};
     for (int i = 0; i < out.n; ++i) {
         for (const View& iv : in)
-            if (views_overlap(out.pages[i], iv)) return fail(CONV_ERR_ALIAS, "pages or scales overlap an input");
+            if (views_overlap(out.pages[i].view, iv)) return fail(CONV_ERR_ALIAS, "pages or scales overlap an input");
         for (int j = 0; j < i; ++j)
-            if (views_overlap(out.pages[i], out.pages[j])) return fail(CONV_ERR_ALIAS, "pages or scales overlap each other");
+            if (grids_overlap(out.pages[i], out.pages[j])) return fail(CONV_ERR_ALIAS, "pages or scales overlap each other");
     }
     if (n_pages == 0) return ok();   // no slot to store to
     KvArgs a = kv_args(p, n_pages, k_pages, v_pages, k_scales, v_scales, k, v);
@@ -272,23 +319,25 @@ conv_status_t kv_cache_load(kv_cache_desc_t desc, int64_t batch, int64_t kv_len,
     const int64_t ks[3] = {kb, p.k_stride, hd}, vs[3] = {vb, p.v_stride, hd};
     if (!nested(ks, batch, kv_len, h, hd) || !nested(vs, batch, kv_len, h, hd))
         return fail(CONV_ERR_ALIAS, "rows of k or v share memory");
-    const KvViews in = kv_views(p, n_pages, k_pages, v_pages, k_scales, v_scales);
+    const KvGrids in = kv_grids(p, n_pages, k_pages, v_pages, k_scales, v_scales);
     // Row by row where all rows are equally far apart, else sequence by
     // sequence, or from the first to the last element.
-    const auto view = [&](const void* q, const int64_t* s) {
-        if (batch == 1 || s[0] == kv_len * s[1]) return rows_view(q, batch * kv_len, s[1], h * hd, es);
+    const auto grid = [&](const void* q, const int64_t* s) {
+        Grid g{(uintptr_t)q, {s[0] * es, s[1] * es, 0}, {batch, kv_len, 1}, h * hd * es, {}};
         const int64_t inner = (kv_len - 1) * s[1] + h * hd;
-        return s[0] >= inner ? View{(uintptr_t)q, batch, s[0] * es, inner * es}
-                             : View{(uintptr_t)q, 1, 0, ((batch - 1) * s[0] + inner) * es};
+        g.view = batch == 1 || s[0] == kv_len * s[1] ? rows_view(q, batch * kv_len, s[1], h * hd, es)
+                 : s[0] >= inner                     ? View{(uintptr_t)q, batch, s[0] * es, inner * es}
+                                                     : View{(uintptr_t)q, 1, 0, ((batch - 1) * s[0] + inner) * es};
+        return g;
     };
-    const View out[2] = {view(k, ks), view(v, vs)};
+    const Grid out[2] = {grid(k, ks), grid(v, vs)};
     const View small[2] = {flat_view(page_table, 4 * batch * max_pages), flat_view(kv_lens, 4 * batch)};
-    if (views_overlap(out[0], out[1])) return fail(CONV_ERR_ALIAS, "k overlaps v");
-    for (const View& ov : out) {
+    if (grids_overlap(out[0], out[1])) return fail(CONV_ERR_ALIAS, "k overlaps v");
+    for (const Grid& o : out) {
         for (int i = 0; i < in.n; ++i)
-            if (views_overlap(ov, in.pages[i])) return fail(CONV_ERR_ALIAS, "k or v overlaps the pages or their scales");
+            if (views_overlap(o.view, in.pages[i].view)) return fail(CONV_ERR_ALIAS, "k or v overlaps the pages or their scales");
         for (const View& s : small)
-            if (views_overlap(ov, s)) return fail(CONV_ERR_ALIAS, "k or v overlaps page_table or kv_lens");
+            if (views_overlap(o.view, s)) return fail(CONV_ERR_ALIAS, "k or v overlaps page_table or kv_lens");
     }
     if (n_pages == 0) return ok();   // no page to read
     KvArgs a = kv_args(p, n_pages, k_pages, v_pages, k_scales, v_scales, k, v);

@@ -86,7 +86,10 @@ CONV2D_API void kv_cache_desc_destroy(kv_cache_desc_t d);
  * Errors: INVALID_ARG for a null or misaligned (element size) pointer, tokens
  * or n_pages * page_size outside 0 .. 2^31 - 1; UNSUPPORTED for a tensor beyond
  * 2^44 elements; ALIAS for pages or scales that overlap an input or each other,
- * or whose own elements share memory. */
+ * or whose own elements share memory.  Keys, values and scales may lie in one
+ * buffer, page by page, or in any order (beside each other for each token or head,
+ * say) where their strides are the same in bytes; pages of different strides that
+ * lie in each other's gaps otherwise count as overlapping. */
 CONV2D_API conv_status_t kv_cache_store(kv_cache_desc_t d, int64_t tokens, const void* k, const void* v,
                                         const int32_t* slots, int64_t n_pages, void* k_pages, void* v_pages,
                                         uint8_t* k_scales, uint8_t* v_scales, void* stream);
@@ -98,7 +101,8 @@ CONV2D_API conv_status_t kv_cache_store(kv_cache_desc_t d, int64_t tokens, const
  * that.  Rows from a sequence's length on, and rows of pages outside
  * [0, n_pages), are left as they were.
  * Errors: as kv_cache_store's, with kv_len and max_pages * page_size up to
- * 2^30; ALIAS also for rows of k or v that share memory. */
+ * 2^30; ALIAS also for rows of k or v that share memory; k and v may lie beside
+ * each other row by row at the same strides. */
 CONV2D_API conv_status_t kv_cache_load(kv_cache_desc_t d, int64_t batch, int64_t kv_len, int64_t max_pages,
                                        const int32_t* page_table, const int32_t* kv_lens, int64_t n_pages,
                                        const void* k_pages, const void* v_pages, const uint8_t* k_scales,

@@ -196,3 +196,51 @@ def test_single_tokens_of_any_batch_are_divided(batch, cache):
     m = cc()
     d = m.paged_attention_desc_create(m.make_paged_attention_params(32, 8, 128, 16, dtype="bf16", cache_dtype=cache))
     assert m.paged_attention_workspace_bytes(d, batch, batch, 8192) > 0
+
+
+def _kv(heads, d, ps, **kw):
+    m = cc()
+    return m.kv_cache_desc_create(m.make_kv_cache_params(heads, d, ps, dtype="bf16", cache_dtype="e4m3", **kw))
+
+
+# (strides of keys and values, of the scales, where values and the two scales begin behind the keys) of pages of 8
+# tokens, 4 heads of 64 codes.
+INTERLEAVED = {
+    "keys and values a token": ((4096, 512, 64), None, (256, P, 2 * P)),
+    "keys and values a head": ((4096, 512, 128), None, (64, P, 2 * P)),
+    "heads outermost": ((512, 64, 1 << 20), None, (1 << 19, P, 2 * P)),
+    "scales behind their rows": ((2560, 320, 80), (2560, 320, 80), (P, 64, P + 64)),
+    "all of a head together": ((5120, 640, 160), (5120, 640, 160), (80, 64, 144)),
+}
+
+
+@pytest.mark.parametrize("name", INTERLEAVED)
+def test_interleaved_pages_do_not_overlap(name):
+    """Rows in each other's gaps are no overlap; a row that reaches one byte into another is.  The last check, of the
+    values' scales against the slots, refuses each call before any launch."""
+    m = cc()
+    strides, scales, (dv, dks, dvs) = INTERLEAVED[name]
+    desc = _kv(4, 64, 8, k_page_strides=strides, v_page_strides=strides, scale_strides=scales)
+    k, v, base = 8 * P, 9 * P, P
+    slots = base + dvs + (7 * scales[1] + 3 * scales[2] if scales else 0)   # where the values' scales alone end
+
+    def status(dv=dv, dks=dks, dvs=dvs):
+        return (m._lib.kv_cache_store(desc.handle, 4, k, v, slots, 60, base, base + dv, base + dks, base + dvs, None),
+                m.conv2d_last_error())
+    assert status() == (m.CONV_ERR_ALIAS, "pages or scales overlap an input")
+    for at in (63,) if scales else (63, -63, strides[0] * 59 + strides[1] * 7 + strides[2] * 3 + 63):
+        assert status(dv=at) == (m.CONV_ERR_ALIAS, "pages or scales overlap each other"), at
+    if scales:
+        for change in (dict(dks=63), dict(dks=0), dict(dks=scales[0] * 5 + scales[1] * 3 + 1)):
+            assert status(**change) == (m.CONV_ERR_ALIAS, "pages or scales overlap each other"), change
+
+
+def test_interleaved_rows_of_a_load_do_not_overlap():
+    """Keys and values in token rows of one buffer, sequences padded; refused for the table, which overlaps the values."""
+    m = cc()
+    desc = _kv(4, 64, 8, k_stride=512, v_stride=512, k_batch_stride=512 * 100, v_batch_stride=512 * 100)
+    k, table = 8 * P, 8 * P + 512
+    status = lambda v: (m._lib.kv_cache_load(desc.handle, 3, 90, 12, table, None, 60, P, 2 * P, 3 * P, 4 * P, k, v, None),  # noqa: E731
+                        m.conv2d_last_error())
+    assert status(k + 512) == (m.CONV_ERR_ALIAS, "k or v overlaps page_table or kv_lens")
+    assert status(k + 510) == (m.CONV_ERR_ALIAS, "k overlaps v") and status(k + 2 * 51200 * 2) == (m.CONV_ERR_ALIAS, "k overlaps v")
