@@ -50,6 +50,7 @@ __global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_ti
     // A score x follows from what its register holds, u: PLAIN, x = scale u;
     // TURNED, x = cap (1 - 2 u); else x = u.
     constexpr bool PLAIN = !CAP, TURNED = CAP == kCapTurned;
+    constexpr bool SIGNED = HALF && DP > 128;   // how a weight's two parts are told apart, see walk
     __shared__ __align__(1024) u32x4 lds[P::S * C::STAGE];
     __shared__ PagedLine line;
     // The last even and odd block that held infinities or NaN.
@@ -221,6 +222,11 @@ __global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_ti
         // in the loop exponentials and products do not overlap across it (chunks
         // among single tokens 58.4 us, 56.2 with two loops, 55.2 all of one part; under a
         // window 40.8, 39.1, 38.6).
+        //
+        // SIGNED: two loops need more registers than 256 wide heads leave.  One
+        // expression forms a weight, the first part's negative or the second part
+        // (1024 tokens over 16384 keys of 16 heads over 4, E4M3: 653 us, 640 without
+        // parts, 725 with two loops, 867 with a branch; bf16: 489, 470, 504, 482).
         const auto walk = [&](auto parts) {
             for (int i = first, stage = 0; i < last; ++i, stage ^= 1) {
                 const int k0 = key0(i);
@@ -316,17 +322,36 @@ __global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_ti
                     for (int d = 0; d < DT; ++d) o[d] *= fade;
                 }
                 const float base = a0 - (m_run == -INFINITY ? 0.0f : m_run);   // nothing seen yet: every weight is 0
-                bf16x8 p[2 * TK];
 #pragma unroll
-                for (int t = 0; t < 2 * TK; ++t)
+                for (int t = 0; t < TK; ++t)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float w = __builtin_amdgcn_exp2f(s[t >> 1][8 * (t & 1) + j] * a1 + base);
-                        s[t >> 1][8 * (t & 1) + j] = w;
-                        l_run += w;
-                        if (HALF) p[t][j] = (bf16)(parts ? weight_part(w, n & 16) : w);
+                    for (int j = 0; j < 16; ++j) {
+                        s[t][j] = __builtin_amdgcn_exp2f(s[t][j] * a1 + base);
+                        l_run += s[t][j];
                     }
+                if constexpr (SIGNED) {
+                    // w, or -(w cut off) in lanes 0 .. 15 and the rest of w in 16 .. 31.
+                    const float keep = !parts ? 1.0f : n & 16 ? 1.0f + 0x1p-20f : 0.0f;
+                    const uint32_t mask = parts ? 0xffff0000u : 0u;
+#pragma unroll
+                    for (int t = 0; t < TK; ++t)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float w = s[t][j];
+                            s[t][j] = __builtin_fmaf(w, keep, -__builtin_bit_cast(float, __builtin_bit_cast(uint32_t, w) & mask));
+                        }
+                } else if (HALF && parts) {
+#pragma unroll
+                    for (int t = 0; t < TK; ++t)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) s[t][j] = weight_part(s[t][j], n & 16);
+                }
                 if constexpr (HALF) {
+                    bf16x8 p[2 * TK];
+#pragma unroll
+                    for (int t = 0; t < 2 * TK; ++t)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) p[t][j] = (bf16)s[t >> 1][8 * (t & 1) + j];
 #pragma unroll
                     for (int t = 0; t < 2 * TK; ++t)
 #pragma unroll
@@ -343,7 +368,8 @@ __global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_ti
 #pragma unroll 1
                     for (int j = 0; j < 32 * TK; ++j) {
                         if (kw + j >= sq.nk || !(now >> (kpart * 32 * TK + j) & 1)) continue;
-                        const bool add = kw + j < hi && (kw + j >= lo || kw + j < a.sinks);
+                        bool add = kw + j < hi && (kw + j >= lo || kw + j < a.sinks);
+                        if (SIGNED && fine && n < 16) add = false;   // the second part's lanes do
 #pragma unroll 1
                         for (int e0 = 0; e0 < a.d; e0 += 64) {
                             const float x = e0 + lane < a.d ? value_at<T, E4>(a, table, h, kw + j, e0 + lane) : 0.0f;
@@ -362,13 +388,13 @@ __global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_ti
                 }
             }
         };
-        if constexpr (HALF) {
+        if constexpr (HALF && !SIGNED) {
             if (fine)
                 walk(std::true_type{});
             else
                 walk(std::false_type{});
         } else {
-            walk(std::false_type{});
+            walk(fine);
         }
         {
             float u, v;
@@ -408,7 +434,7 @@ __global__ __launch_bounds__(256, (PagedTile<T, DP, KW, E4>::OCC)) void paged_ti
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
-                for (int q = 0; q < 16; ++q) o[d][q] = both_rows(o[d][q]);
+                for (int q = 0; q < 16; ++q) o[d][q] = both_rows(SIGNED && n < 16 ? -o[d][q] : o[d][q]);
         }
         if (!live || (fine && n >= 16)) continue;
         const PagedArgs& end = kernel_args();

@@ -94,3 +94,33 @@ def test_short_sequences_keep_16_bits(softcap, d, cache, batch):
             fine += want.numel()
     assert fine and (softcap or coarse > fine // 100)
 
+
+
+@pytest.mark.parametrize("batch", ["alone", "in 64", "in 128", "whole"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+def test_seen_infinities_of_short_sequences(value, d, batch):
+    """An element among keys that every row sees, and one that the last row alone sees: they reach that element, with
+    their sign, and no other."""
+    q_lens = BATCHES[batch]
+    hk, group, ps = 16 if batch == "whole" else 2, 4, 16
+    lens = [n + 150 for n in q_lens]
+    n_pages = max(-(-n // ps) for n in lens) + 2
+    pages, scales, values = _cache(n_pages, ps, hk, d, "bf16", d)
+    table = torch.arange(n_pages, dtype=torch.int32).expand(len(lens), -1).contiguous()
+    short = [b for b, n in enumerate(q_lens) if 2 <= n <= 4][0]
+    last = lens[short] - 1
+    pages[1].view(-1, hk, d)[3, 0, 5] = value
+    pages[1].view(-1, hk, d)[last, 1, d - 7] = value
+    q = torch.zeros(sum(q_lens), hk * group, d)
+    q.view(-1, d)[torch.arange(q.numel() // d), torch.arange(q.numel() // d) * 7 % d] = 1.0
+    out = _run(q.to(BF16), q_lens, lens, table, pages, scales, hk, "bf16", scale=1.5)
+    first = sum(q_lens[:short])
+    for i in range(q_lens[short]):
+        row, want = out[first + i], torch.zeros(hk * group, d, dtype=torch.float64)
+        want[:group, 5] = value
+        if i == q_lens[short] - 1:
+            want[group:2 * group, d - 7] = value
+        fine = torch.isfinite(want)
+        assert torch.isfinite(row[fine]).all()
+        assert torch.isnan(row[~fine]).all() if value != value else (row[~fine] == value).all()
