@@ -1,5 +1,7 @@
 // The norm behind a block, its gate and the scaled residual, and the norm
 // before the next block, a row at a time.
+#include <cfloat>
+
 #include "decoder_internal.h"
 #include "seq_common.h"
 
@@ -41,6 +43,20 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
     return s;
 }
 
+// A row's squares may leave fp32's range where the row does not: then they are
+// formed of the row times a power of two.  2^-80 brings the largest squares and sums
+// of 32768 elements into range, 2^64 the least ones (which count only where no
+// eps outweighs them).
+constexpr float kDown = 0x1p-80f, kUp = 0x1p64f;
+__device__ __forceinline__ bool out_of_range(float total, float eps) {
+    return !(total < INFINITY) || (total < 0x1p-80f && eps < 0x1p-100f);
+}
+// What eps is next to the squares of a row times `scale`; above zero where it is,
+// so that a row without spread stays 0.
+__device__ __forceinline__ float scaled_eps(float eps, float scale) {
+    return eps > 0.0f ? fmaxf(eps * scale * scale, FLT_MIN) : 0.0f;
+}
+
 // NW waves a row, whose pieces stay in registers, CP of them a thread: every
 // element is read once and written once, and a row's mean is known before the
 // squares around it are summed.  With up to 8 elements a thread a workgroup
@@ -73,22 +89,41 @@ __global__ __launch_bounds__(64 * NW) void block_norm(NormArgs a) {
     }
     // The norm of the pieces in place.
     const auto norm = [&](Piece<V> (&p)[CP], int kind, int which) {
+        float unit = 1.0f;
         if (kind == BLOCK_NORM_LAYER) {
-            float s = 0.0f;
+            const auto sum = [&](float scale) {
+                float s = 0.0f;
+#pragma unroll
+                for (int c = 0; c < CP; ++c)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) s += scale * p[c][i];   // zeros past the row
+                return block_sum<NW>(s, part[2 * which]);
+            };
+            // Halves: an element less the mean may be beyond fp32's range.
+            unit = 0.5f;
+            float half_mean = sum(1.0f) * inv_n * 0.5f;
+            if (!(fabsf(half_mean) < INFINITY)) {
+                if (NW > 1) __syncthreads();   // the sums have been read
+                half_mean = sum(kDown) * inv_n * (0.5f / kDown);
+            }
+#pragma unroll
+            for (int c = 0; c < CP; ++c) p[c] = on(c) ? 0.5f * p[c] - half_mean : Piece<V>(0.0f);
+        }
+        const auto squares = [&](float scale) {
+            float sq = 0.0f;
 #pragma unroll
             for (int c = 0; c < CP; ++c)
 #pragma unroll
-                for (int i = 0; i < V; ++i) s += p[c][i];   // zeros past the row
-            const float mean = block_sum<NW>(s, part[2 * which]) * inv_n;
-#pragma unroll
-            for (int c = 0; c < CP; ++c) p[c] = on(c) ? p[c] - mean : Piece<V>(0.0f);
+                for (int i = 0; i < V; ++i) sq += (scale * p[c][i]) * (scale * p[c][i]);
+            return block_sum<NW>(sq, part[2 * which + 1]);
+        };
+        float total = squares(1.0f), scale = 1.0f;
+        if (out_of_range(total, a.eps)) {
+            scale = total < 1.0f ? kUp : kDown;
+            if (NW > 1) __syncthreads();   // the sums have been read
+            total = squares(scale);
         }
-        float sq = 0.0f;
-#pragma unroll
-        for (int c = 0; c < CP; ++c)
-#pragma unroll
-            for (int i = 0; i < V; ++i) sq += p[c][i] * p[c][i];
-        const float r = 1.0f / sqrtf(block_sum<NW>(sq, part[2 * which + 1]) * inv_n + a.eps);
+        const float r = scale / sqrtf(total * inv_n + scaled_eps(a.eps, unit * scale));
 #pragma unroll
         for (int c = 0; c < CP; ++c) {
             if constexpr (HOLD)
@@ -163,14 +198,24 @@ __global__ __launch_bounds__(1024) void block_norm_wide(NormArgs a) {
     const float inv_n = 1.0f / (float)a.width;
     // Each thread keeps to its own elements.
     const auto norm = [&](int kind, const float* gamma, const float* beta, float (*sums)[16]) {
-        float mean = 0.0f, sq = 0.0f;
-        if (kind == BLOCK_NORM_LAYER) {
-            float s = 0.0f;
-            for (int e = tid; e < a.width; e += 1024) s += v[e];
-            mean = block_sum<16>(s, sums[0]) * inv_n;
+        float mean, total, eps = a.eps;
+        for (bool again = false;; again = true) {
+            mean = 0.0f;
+            if (kind == BLOCK_NORM_LAYER) {
+                float s = 0.0f;
+                for (int e = tid; e < a.width; e += 1024) s += v[e];
+                mean = block_sum<16>(s, sums[0]) * inv_n;
+            }
+            float sq = 0.0f;
+            for (int e = tid; e < a.width; e += 1024) sq += (v[e] - mean) * (v[e] - mean);
+            total = block_sum<16>(sq, sums[1]);
+            if (again || !out_of_range(total, eps)) break;
+            const float scale = total < 1.0f ? kUp : kDown;
+            for (int e = tid; e < a.width; e += 1024) v[e] *= scale;
+            eps = scaled_eps(eps, scale);
+            __syncthreads();   // the sums have been read
         }
-        for (int e = tid; e < a.width; e += 1024) sq += (v[e] - mean) * (v[e] - mean);
-        const float r = 1.0f / sqrtf(block_sum<16>(sq, sums[1]) * inv_n + a.eps);
+        const float r = 1.0f / sqrtf(total * inv_n + eps);
         for (int e = tid; e < a.width; e += 1024) v[e] = (v[e] - mean) * r * gamma[e] + (beta ? beta[e] : 0.0f);
     };
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {

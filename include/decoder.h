@@ -219,7 +219,9 @@ CONV2D_API void block_norm_desc_destroy(block_norm_desc_t d);
  * and pre_gamma float32[width], required iff there is that norm; the betas
  * float32[width], required iff they are set; gate [ceil(rows / gate_rows)]
  * [width], required iff has_gate; out required iff there is a pre norm, and
- * unused otherwise.  Sums are fp32, LAYER's around the row's mean.
+ * unused otherwise.  Sums are fp32, LAYER's around the row's mean; where a row's
+ * squares or their sum would leave fp32's range, the row is scaled for them by a
+ * power of two.
  * residual may be x or y itself (same pointer and stride), out may be y itself;
  * any other overlap of residual or out with an input or with each other returns
  * ALIAS.  INVALID_ARG for a null or misaligned pointer, rows < 0 or > 2^31 - 1;
