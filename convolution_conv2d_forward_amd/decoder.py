@@ -4,8 +4,8 @@ Argument marshalling only, as in attention.py: torch tensors give device memory
 and the current stream, compiled checks (_marshal) hold device, type, shape and
 strides against the descriptor, and raw pointers go through the C ABI.  Sizes
 that a call may change (tokens, batch, rows, pages) come from the tensors'
-shapes.  All tensors of a call lie on the current device, or, where a stream is
-given, on the stream's.
+shapes.  All tensors of a call lie on the current device, and so does the stream:
+a torch stream of another device is refused; of a raw handle it is not known.
 
     d = kv_cache_desc_create(make_kv_cache_params(8, 128, 16, dtype="bf16", cache_dtype="e4m3"))
     kv_cache_store(d, k, v, slots, k_pages, v_pages, k_scales, v_scales)

@@ -32,8 +32,11 @@
  * Cache types: the call's own dtype (CONV_DTYPE_F32 or CONV_DTYPE_BF16), or
  * KV_CACHE_E4M3: a code of 8 bits an element (1 sign, 4 exponent, 3 mantissa
  * bits; largest number 448, no infinities) and a scale byte a token and head,
- * so that an element is code * 2^(scale - 127).  Dequantised elements are exact
- * in either dtype.
+ * so that an element is code * 2^(scale - 127).  Elements dequantised with the
+ * scales that kv_cache_store writes (10 .. 246) are exact in either dtype; other
+ * scales are not for these operators.  kv_cache_store and kv_cache_load take heads
+ * of any width, paged_attention_forward those whose rows in the pages are multiples
+ * of 16 bytes (16 codes).
  */
 #ifndef DECODER_MI355X_H
 #define DECODER_MI355X_H
@@ -157,8 +160,7 @@ CONV2D_API conv_status_t paged_attention_workspace_bytes(paged_attention_desc_t 
  * are not read.  Scores are scale * q.k, capped.  Rows that see no key are
  * zero.  Rows of out that belong to no sequence are left as they were; two
  * sequences must not share rows.  Elements of k and v that a row does not see
- * do not reach it, whatever they hold, and scale bytes that a row sees are
- * those that kv_cache_store writes (10 .. 246).  An infinity that a row sees
+ * do not reach it, whatever they and their scales hold.  An infinity that a row sees
  * makes that element of the row infinite (NaN, as 0 * inf, where its weight is
  * below fp32's range).
  *   workspace   at least paged_attention_workspace_bytes, 16-byte aligned,

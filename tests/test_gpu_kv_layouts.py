@@ -45,7 +45,6 @@ def test_interleaved(layout, dtype, cache):
         k, v = k.view(E4M3), v.view(E4M3)
     slots = torch.randperm(PAGES * PS, generator=g)
     x = torch.randn(2, PAGES * PS, HEADS, D, generator=g).to(t)
-    # Rows of keys and values beside each other, in a buffer that is wider: the batch of one, and of two padded ones.
     ints = lambda a: torch.as_tensor(a, dtype=torch.int32).cuda()  # noqa: E731
     desc = m.kv_cache_desc_create(m.make_kv_cache_params(HEADS, D, PS, dtype=dtype, cache_dtype=cache, **strides))
     m.kv_cache_store(desc, x[0].cuda(), x[1].cuda(), ints(slots), k, v, *scales)
