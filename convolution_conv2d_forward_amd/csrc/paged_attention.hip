@@ -202,8 +202,8 @@ PagedPlan plan_paged_attention(int32_t dtype, bool e4m3, const PagedArgs& a) {
     p.group_heads = pair ? 2 : 1;
     if (pair) keys /= 2;
     // Fewer (tile, group)s than two rounds of workgroups are divided.  (A prompt
-    // of 8192 tokens, two rounds of them: 364 us divided, 316 whole; one of 4096,
-    // one round: 114 and 141.  A token of 128 sequences of up to 2048 keys, two
+    // of 8192 tokens, two rounds of them: 364 us divided, 316 whole, 450 and 369 with
+    // cold inputs; one of 4096, one round: 114 and 141.  A token of 128 sequences of up to 2048 keys, two
     // rounds: 149 and 143; of 192, one and a half: 122 and 135.)
     //
     // Of more tiles of 16 rows those of more than 2048 keys are, since one sequence
